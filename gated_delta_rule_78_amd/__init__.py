@@ -18,6 +18,8 @@ __all__ = ["chunk_fwd", "chunk_records", "chunk_apply_records", "chunk_fwd_debug
            "gdn2_chunk_fwd", "gdn2_decode_step", "decode_tokens", "gdn2_decode_tokens", "chunk_fwd_varlen",
            "sfda_chunk_fwd", "sfda_decode_step", "sfda_decode_tokens", "chunk_bwd", "chunk_bwd_varlen",
            "gdn2_chunk_bwd", "bwd_workspace_size",
+           "lina_chunk_fwd", "lina_chunk_bwd", "lina_decode_step", "lina_decode_tokens",
+           "qk_norm_rope", "qk_norm_rope_bwd", "rope_inv_freq",
            "workspace_size", "pick_path", "chunk_fwd_noalloc", "lib", "version", "status_string",
            "LIB_PATH", "KdaError", "Shape", "BF16", "F32"]
 
@@ -36,6 +38,14 @@ class KdaError(RuntimeError):
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("dk", ctypes.c_int),
                 ("dv", ctypes.c_int), ("chunk", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_longlong), ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int),
+                ("d", ctypes.c_int), ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("positions_64", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 def lib() -> ctypes.CDLL:
@@ -110,6 +120,34 @@ def lib() -> ctypes.CDLL:
         L.kda_sfda_chunk_bwd_varlen.argtypes = [SP, P, ctypes.c_int, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P,
                                                 ctypes.c_size_t, P]
         L.kda_sfda_chunk_bwd_varlen.restype = ctypes.c_int
+        I, Z = ctypes.c_int, ctypes.c_size_t
+        L.kda_lina_chunk_fwd_workspace_size.argtypes = [SP]
+        L.kda_lina_chunk_fwd_workspace_size.restype = Z
+        L.kda_lina_chunk_fwd.argtypes = [SP, I, P, P, P, P, I, P, P, P, P, Z, P]
+        L.kda_lina_chunk_fwd.restype = I
+        L.kda_lina_chunk_fwd_varlen_workspace_size.argtypes = [SP, I]
+        L.kda_lina_chunk_fwd_varlen_workspace_size.restype = Z
+        L.kda_lina_chunk_fwd_varlen.argtypes = [SP, I, P, I, P, P, P, P, I, P, P, P, P, Z, P]
+        L.kda_lina_chunk_fwd_varlen.restype = I
+        L.kda_lina_chunk_bwd_workspace_size.argtypes = [SP, I]
+        L.kda_lina_chunk_bwd_workspace_size.restype = Z
+        L.kda_lina_chunk_bwd.argtypes = [SP, I, P, P, P, P, I] + [P] * 9 + [Z, P]
+        L.kda_lina_chunk_bwd.restype = I
+        L.kda_lina_chunk_bwd_varlen_workspace_size.argtypes = [SP, I, I]
+        L.kda_lina_chunk_bwd_varlen_workspace_size.restype = Z
+        L.kda_lina_chunk_bwd_varlen.argtypes = [SP, I, P, I, P, P, P, P, I] + [P] * 9 + [Z, P]
+        L.kda_lina_chunk_bwd_varlen.restype = I
+        L.kda_lina_decode_step.argtypes = [SP, I, P, P, P, P, I, P, P, P]
+        L.kda_lina_decode_step.restype = I
+        L.kda_lina_decode_tokens.argtypes = [SP, I, P, P, P, P, I, P, P, P]
+        L.kda_lina_decode_tokens.restype = I
+        QP = ctypes.POINTER(QkShape)
+        L.kda_qk_norm_rope.argtypes = [QP] + [P] * 9
+        L.kda_qk_norm_rope.restype = I
+        L.kda_qk_norm_rope_bwd_workspace_size.argtypes = [QP]
+        L.kda_qk_norm_rope_bwd_workspace_size.restype = Z
+        L.kda_qk_norm_rope_bwd.argtypes = [QP] + [P] * 13 + [Z, P]
+        L.kda_qk_norm_rope_bwd.restype = I
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_version.argtypes = []
@@ -666,3 +704,7 @@ def sfda_chunk_bwd(q, k, v, lam, beta, d_o, initial_state=None, d_final_state=No
     channels."""
     return _bwd_call(q, k, v, lam, (beta,), d_o, cu_seqlens, initial_state, d_final_state, want_d_initial,
                      workspace, family="sfda")
+
+
+from .lina import lina_chunk_bwd, lina_chunk_fwd, lina_decode_step, lina_decode_tokens  # noqa: E402
+from .qk import qk_norm_rope, qk_norm_rope_bwd, rope_inv_freq  # noqa: E402

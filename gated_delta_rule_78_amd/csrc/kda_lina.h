@@ -1,0 +1,72 @@
+// kda_lina.h -- arguments of the linear-attention kernels (decay per head), shared by the
+// C ABI (kda_lina_api.cpp) and the launchers (kda_lina.hip, kda_lina_decode.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+// An operand of a walk: [rows, heads, dim] with head h of H mapped to h / (H / heads).
+struct LinaOp {
+  const void* p = nullptr;
+  int heads = 0;
+};
+
+enum LinaDot : int { kDotNone = 0, kDotRow = 1, kDotCross = 2 };
+
+// One walk  out_i = sum_{j <= i} r_ij (Q_i . K_j) V_j  (+ the start state's part), tokens in
+// order or (rev) in reverse order.
+struct LinaWalk {
+  LinaOp q, k, v, x;      // x: what the walk's dots are taken with (dot != kDotNone)
+  void* out = nullptr;    // [rows, H, dv], element type of q, or fp32 when out_f32
+  bool out_f32 = false;
+  const float* g = nullptr;
+  bool g_fixed = false;   // g is [H] instead of [rows, H]
+  const float* s0 = nullptr;  // [n, H, dk, dv] (s_t: [n, H, dv, dk]) or NULL
+  float* sT = nullptr;
+  bool s_t = false;
+  bool rev = false;
+  int dot = kDotNone;
+  float* dots = nullptr;      // [dv / 64][H][rows] fp32
+  float* snap = nullptr;      // states every kLinaGroup chunks (forward walk with kDotRow writes them)
+  float* anchor = nullptr;    // [groups][H][dv / 64] (reverse walk with kDotRow: <snap, state>)
+  float* seg_state = nullptr; // [segments][H][dv / 64][dk * 64]
+  float* seg_dec = nullptr;   // [segments][H]
+  // batch
+  const int* cs = nullptr;    // clamped offsets of a packed batch [n + 1], or NULL
+  int n = 0;                  // sequences
+  int T = 0;                  // tokens of each sequence (packed: of the batch)
+  int H = 0, dk = 0, dv = 0;  // the walk's own widths: Q, K have dk channels, V, out dv
+  int L = 0;                  // chunks of a segment
+  bool split = false;         // segments are walked apart (L < the longest chain)
+  bool bf16 = true;
+  void* stream = nullptr;
+};
+
+constexpr int kLinaGroup = 16;  // chunks between two kept states of the backward
+
+// Segments (or groups of `per` chunks) of a batch: sequence i starts at
+// offset / (64 per) + i, so that every sequence has at least one.
+inline int64_t lina_pieces(int64_t rows, int64_t n, int64_t per) { return rows / (64 * per) + n; }
+
+hipError_t launch_lina_walk(const LinaWalk& w);
+hipError_t launch_lina_offsets(const int* cu, int n, int T, int* cs, void* stream);
+hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int heads, int group, int d, bool bf16,
+                               void* stream);
+hipError_t launch_lina_ddecay(const LinaWalk& w, const float* a, const float* b, const float* e, int na, int ne,
+                              const float* anchor, float* dg, double* part, float* dg_fixed);
+
+struct LinaDecodeArgs {
+  const void *q, *k, *v;
+  const float* g;
+  bool g_fixed;
+  float* state;
+  void* o;
+  int64_t BH;
+  int ntok, H, Hk, dk, dv;
+  bool bf16;
+  void* stream;
+};
+hipError_t launch_lina_decode(const LinaDecodeArgs& a);
+
+}  // namespace kda

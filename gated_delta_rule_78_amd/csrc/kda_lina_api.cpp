@@ -1,0 +1,388 @@
+// kda_lina_api.cpp -- C ABI of linear attention with a decay per head (include/kda.h,
+// kda_lina_*): argument checks on the host, then the walks' launches.
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/kda.h"
+#include "kda_check.h"
+#include "kda_lina.h"
+
+namespace {
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_lina_shape(const kda_shape* s, int qk_heads, bool decode, int n_seqs, int* es) {
+  if (!s) return KDA_ERR_NULL;
+  if (s->dtype != KDA_BF16 && s->dtype != KDA_F32) return KDA_ERR_DTYPE;
+  if (s->B < 0 || s->H < 1 || s->H > 65535 || qk_heads < 1 || s->dk < 1 || s->dv < 1 || (!decode && s->T < 0))
+    return KDA_ERR_SHAPE;
+  if (s->H % qk_heads != 0) return KDA_ERR_SHAPE;
+  if (n_seqs >= 0 && (s->B != 1 || n_seqs > (1 << 24))) return KDA_ERR_SHAPE;
+  const int64_t rows = (int64_t)s->B * (decode && s->T < 1 ? 1 : s->T) * s->H;
+  if (rows > (int64_t(1) << 40) / 256) return KDA_ERR_SHAPE;
+  if (!supported_width(s->dk) || !supported_width(s->dv)) return KDA_ERR_UNSUPPORTED;
+  if (!decode && s->chunk != 0 && s->chunk != 64) return KDA_ERR_UNSUPPORTED;
+  *es = s->dtype == KDA_BF16 ? 2 : 4;
+  return KDA_OK;
+}
+
+// Chunks of a segment.  A chain (sequence, head, 64 value columns) is walked in order; with
+// fewer chains than compute units it is cut into segments, whose start states cost one more
+// read of k and v.
+struct Plan {
+  int L;
+  bool split;
+  int64_t nseg;
+};
+
+Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
+  const bool packed = n_seqs >= 0;
+  const int64_t nch = std::max<int64_t>(1, ((int64_t)s.T + 63) / 64);
+  const int64_t n = packed ? n_seqs : s.B;
+  const int64_t chains = std::max<int64_t>(1, n * s.H * nv);
+  const int64_t work = (packed ? nch + n : nch * n) * s.H * nv;  // chunk steps in all
+  int64_t L = nch;
+  if (packed || chains < 256) L = std::max<int64_t>(16, (work + 511) / 512);
+  L = std::min(L, nch);
+  Plan p;
+  p.L = (int)L;
+  p.split = L < nch;
+  p.nseg = packed ? kda::lina_pieces(s.T, n, L) : n * ((nch + L - 1) / L);
+  return p;
+}
+
+struct FwdLayout {
+  Plan plan;
+  size_t off_dec, off_cs, bytes;
+};
+
+FwdLayout fwd_layout(const kda_shape& s, int n_seqs) {
+  FwdLayout l;
+  l.plan = lina_plan(s, n_seqs, s.dv / 64);
+  const size_t seg = l.plan.split ? (size_t)l.plan.nseg : 0;
+  l.off_dec = up(seg * s.H * s.dk * s.dv * 4);
+  l.off_cs = up(l.off_dec + seg * s.H * 4);
+  l.bytes = n_seqs >= 0 ? up(l.off_cs + ((size_t)n_seqs + 1) * 4) : l.off_cs;
+  return l;
+}
+
+int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const void* q, const void* k, const void* v,
+             const float* g, int per_head, const float* s0, void* o, float* sT, void* ws, size_t ws_bytes,
+             void* stream) {
+  int es = 0;
+  int rc = check_lina_shape(shape, Hk, false, n_seqs, &es);
+  if (rc) return rc;
+  const kda_shape& s = *shape;
+  const bool packed = n_seqs >= 0;
+  if (packed && !cu) return KDA_ERR_NULL;
+  const int64_t n = packed ? n_seqs : s.B, toks = (int64_t)s.B * s.T;
+  if (toks > 0 && (!q || !k || !v || !g || !o)) return KDA_ERR_NULL;
+  for (const void* x : {q, k, v, (const void*)o, (const void*)s0, (const void*)sT})
+    if (x && misaligned(x)) return KDA_ERR_ALIGN;
+  if (misaligned(g, 4) || misaligned(cu, 4)) return KDA_ERR_ALIGN;
+  const FwdLayout l = fwd_layout(s, n_seqs);
+  if (l.bytes > 0 && !ws) return KDA_ERR_NULL;
+  if (ws_bytes < l.bytes) return KDA_ERR_WORKSPACE;
+  if (misaligned(ws, 256)) return KDA_ERR_ALIGN;
+  const int64_t st = n * s.H * s.dk * s.dv * 4;
+  const Range in[] = {range_of(q, q ? toks * Hk * s.dk * es : 0), range_of(k, k ? toks * Hk * s.dk * es : 0),
+                      range_of(v, v ? toks * s.H * s.dv * es : 0),
+                      range_of(g, g ? (per_head ? (int64_t)s.H : toks * s.H) * 4 : 0),
+                      range_of(cu, packed ? (int64_t)(n_seqs + 1) * 4 : 0), range_of(s0, s0 ? st : 0)};
+  const Range out[] = {range_of(o, o ? toks * s.H * s.dv * es : 0), range_of(sT, sT ? st : 0),
+                       range_of(ws, (int64_t)l.bytes)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 6; ++j)
+      if (overlap(out[i], in[j]) && !(i == 1 && j == 5 && s0 == sT)) return KDA_ERR_ALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(out[i], out[j])) return KDA_ERR_ALIAS;
+  }
+  if (n == 0) return KDA_OK;
+  char* w = (char*)ws;
+  kda::LinaWalk a;
+  a.q = {q, Hk};
+  a.k = {k, Hk};
+  a.v = {v, s.H};
+  a.out = o;
+  a.g = g;
+  a.g_fixed = per_head != 0;
+  a.s0 = s0;
+  a.sT = sT;
+  a.n = (int)n;
+  a.T = s.T;
+  a.H = s.H;
+  a.dk = s.dk;
+  a.dv = s.dv;
+  a.L = l.plan.L;
+  a.split = l.plan.split;
+  a.seg_state = (float*)w;
+  a.seg_dec = (float*)(w + l.off_dec);
+  a.bf16 = s.dtype == KDA_BF16;
+  a.stream = stream;
+  if (packed) {
+    a.cs = (const int*)(w + l.off_cs);
+    if (kda::launch_lina_offsets(cu, n_seqs, s.T, (int*)(w + l.off_cs), stream) != hipSuccess) return KDA_ERR_HIP;
+  }
+  return kda::launch_lina_walk(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+// Workspace of the backward: segment states (the three walks use them in turn), kept states
+// and per-token parts of the decay gradient, the per-head gradients of shared q and k.
+struct BwdLayout {
+  Plan plan;
+  int64_t groups;
+  size_t off_dec, off_cs, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
+};
+
+BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
+  BwdLayout l;
+  const int64_t n = n_seqs >= 0 ? n_seqs : s.B, toks = (int64_t)s.B * s.T;
+  l.plan = lina_plan(s, n_seqs, std::min(s.dk, s.dv) / 64);
+  const size_t seg = l.plan.split ? (size_t)l.plan.nseg : 0, state = (size_t)s.H * s.dk * s.dv * 4;
+  const int64_t per = 64 * kda::kLinaGroup;
+  l.groups = n_seqs >= 0 ? kda::lina_pieces(s.T, n, kda::kLinaGroup) : n * ((s.T + per - 1) / per);
+  l.off_dec = up(seg * state);
+  l.off_cs = up(l.off_dec + seg * s.H * 4);
+  l.off_snap = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
+  l.off_anchor = up(l.off_snap + l.groups * state);
+  l.off_a = up(l.off_anchor + (size_t)l.groups * s.H * (s.dk / 64) * 4);
+  const size_t dots = (size_t)toks * s.H * 4;
+  l.off_b = up(l.off_a + dots * (s.dk / 64));
+  l.off_e = up(l.off_b + dots * (s.dk / 64));
+  l.off_part = up(l.off_e + dots * (s.dv / 64));
+  l.off_share = up(l.off_part + (size_t)l.groups * s.H * 8);
+  l.bytes = up(l.off_share + (s.H > Hk ? (size_t)toks * s.H * s.dk * 4 : 0));
+  return l;
+}
+
+struct BwdPtrs {
+  const void *q, *k, *v;
+  const float* g;
+  int per_head;
+  const float* s0;
+  const void* d_o;
+  const float* dsT;
+  void *dq, *dk, *dv;
+  float *dg, *ds0;
+  void* ws;
+  size_t ws_bytes;
+};
+
+int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const BwdPtrs& p, void* stream) {
+  int es = 0;
+  int rc = check_lina_shape(shape, Hk, false, n_seqs, &es);
+  if (rc) return rc;
+  const kda_shape& s = *shape;
+  const bool packed = n_seqs >= 0;
+  if (packed && !cu) return KDA_ERR_NULL;
+  const int64_t n = packed ? n_seqs : s.B, toks = (int64_t)s.B * s.T;
+  if (toks > 0 && (!p.q || !p.k || !p.v || !p.g || !p.d_o || !p.dq || !p.dk || !p.dv)) return KDA_ERR_NULL;
+  for (const void* x : {p.q, p.k, p.v, p.d_o, (const void*)p.s0, (const void*)p.dsT, (const void*)p.dq,
+                        (const void*)p.dk, (const void*)p.dv, (const void*)p.ds0})
+    if (x && misaligned(x)) return KDA_ERR_ALIGN;
+  if (misaligned(p.g, 4) || misaligned(p.dg, 4) || misaligned(cu, 4)) return KDA_ERR_ALIGN;
+  const BwdLayout l = bwd_layout(s, Hk, n_seqs);
+  if (l.bytes > 0 && !p.ws) return KDA_ERR_NULL;
+  if (p.ws_bytes < l.bytes) return KDA_ERR_WORKSPACE;
+  if (misaligned(p.ws, 256)) return KDA_ERR_ALIGN;
+  const int64_t st = n * s.H * s.dk * s.dv * 4, qk = toks * Hk * s.dk * es, vo = toks * s.H * s.dv * es;
+  const int64_t gb = (p.per_head ? (int64_t)s.H : toks * s.H) * 4;
+  const Range in[] = {range_of(p.q, p.q ? qk : 0),   range_of(p.k, p.k ? qk : 0),     range_of(p.v, p.v ? vo : 0),
+                      range_of(p.g, p.g ? gb : 0),   range_of(p.s0, p.s0 ? st : 0),   range_of(p.d_o, p.d_o ? vo : 0),
+                      range_of(p.dsT, p.dsT ? st : 0), range_of(cu, packed ? (int64_t)(n_seqs + 1) * 4 : 0)};
+  const Range out[] = {range_of(p.dq, p.dq ? qk : 0), range_of(p.dk, p.dk ? qk : 0), range_of(p.dv, p.dv ? vo : 0),
+                       range_of(p.dg, p.dg ? gb : 0), range_of(p.ds0, p.ds0 ? st : 0),
+                       range_of(p.ws, (int64_t)l.bytes)};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return KDA_ERR_ALIAS;
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(out[i], out[j])) return KDA_ERR_ALIAS;
+  }
+  char* ws = (char*)p.ws;
+  kda::LinaWalk a;
+  a.g = p.g;
+  a.g_fixed = p.per_head != 0;
+  a.n = (int)n;
+  a.T = s.T;
+  a.H = s.H;
+  a.L = l.plan.L;
+  a.split = l.plan.split;
+  a.seg_state = (float*)ws;
+  a.seg_dec = (float*)(ws + l.off_dec);
+  a.bf16 = s.dtype == KDA_BF16;
+  a.stream = stream;
+  if (n == 0 || toks == 0) {
+    // no token: the start state's gradient is the final state's, a fixed decay's is zero
+    if (p.dg && p.per_head && kda::launch_lina_ddecay(a, nullptr, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr,
+                                                      p.dg) != hipSuccess)
+      return KDA_ERR_HIP;
+    if (n == 0) return KDA_OK;
+  }
+  if (packed) {
+    a.cs = (const int*)(ws + l.off_cs);
+    if (kda::launch_lina_offsets(cu, n_seqs, s.T, (int*)(ws + l.off_cs), stream) != hipSuccess) return KDA_ERR_HIP;
+  }
+  const bool shared = s.H > Hk;
+  float* share = (float*)(ws + l.off_share);
+  float* anchor = (float*)(ws + l.off_anchor);
+  float *da = (float*)(ws + l.off_a), *db = (float*)(ws + l.off_b), *de = (float*)(ws + l.off_e);
+  const kda::LinaOp q{p.q, Hk}, k{p.k, Hk}, v{p.v, s.H}, u{p.d_o, s.H};
+  if (toks > 0) {
+    kda::LinaWalk w = a;  // dq
+    w.q = u;
+    w.k = v;
+    w.v = k;
+    w.x = q;
+    w.dk = s.dv;
+    w.dv = s.dk;
+    w.out = shared ? (void*)share : p.dq;
+    w.out_f32 = shared;
+    w.s0 = p.s0;
+    w.s_t = true;
+    w.dot = p.dg ? kda::kDotRow : kda::kDotNone;
+    w.dots = da;
+    w.snap = (float*)(ws + l.off_snap);
+    if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
+    if (shared && kda::launch_lina_headsum(share, p.dq, toks, Hk, s.H / Hk, s.dk, a.bf16, stream) != hipSuccess)
+      return KDA_ERR_HIP;
+    // dk
+    w.q = v;
+    w.k = u;
+    w.v = q;
+    w.x = k;
+    w.out = shared ? (void*)share : p.dk;
+    w.s0 = p.dsT;
+    w.rev = true;
+    w.dots = db;
+    w.anchor = anchor;
+    if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
+    if (shared && kda::launch_lina_headsum(share, p.dk, toks, Hk, s.H / Hk, s.dk, a.bf16, stream) != hipSuccess)
+      return KDA_ERR_HIP;
+  }
+  kda::LinaWalk w = a;  // dv and the start state's gradient
+  w.q = k;
+  w.k = q;
+  w.v = u;
+  w.x = v;
+  w.dk = s.dk;
+  w.dv = s.dv;
+  w.out = p.dv;
+  w.s0 = p.dsT;
+  w.sT = p.ds0;
+  w.rev = true;
+  w.dot = p.dg ? kda::kDotCross : kda::kDotNone;
+  w.dots = de;
+  if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
+  if (p.dg && toks > 0 &&
+      kda::launch_lina_ddecay(w, da, db, de, s.dk / 64, s.dv / 64, anchor, p.per_head ? nullptr : p.dg,
+                              (double*)(ws + l.off_part), p.per_head ? p.dg : nullptr) != hipSuccess)
+    return KDA_ERR_HIP;
+  return KDA_OK;
+}
+
+int decode_impl(const kda_shape* shape, int Hk, int ntok, const void* q, const void* k, const void* v, const float* g,
+                int per_head, float* state, void* o, void* stream) {
+  if (!shape) return KDA_ERR_NULL;
+  kda_shape s = *shape;
+  s.T = ntok;
+  int es = 0;
+  int rc = check_lina_shape(&s, Hk, true, -1, &es);
+  if (rc) return rc;
+  if (ntok < 0) return KDA_ERR_SHAPE;
+  const int64_t toks = (int64_t)s.B * ntok, st = (int64_t)s.B * s.H * s.dk * s.dv * 4;
+  if (toks > 0 && (!q || !k || !v || !g || !state || !o)) return KDA_ERR_NULL;
+  if (state && misaligned(state)) return KDA_ERR_ALIGN;
+  if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(o, es) || misaligned(g, 4))
+    return KDA_ERR_ALIGN;
+  const Range in[] = {range_of(q, q ? toks * Hk * s.dk * es : 0), range_of(k, k ? toks * Hk * s.dk * es : 0),
+                      range_of(v, v ? toks * s.H * s.dv * es : 0),
+                      range_of(g, g ? (per_head ? (int64_t)s.H : toks * s.H) * 4 : 0)};
+  const Range ro = range_of(o, o ? toks * s.H * s.dv * es : 0), rs = range_of(state, state ? st : 0);
+  for (const Range& r : in)
+    if (overlap(ro, r) || overlap(rs, r)) return KDA_ERR_ALIAS;
+  if (overlap(ro, rs)) return KDA_ERR_ALIAS;
+  if (toks == 0) return KDA_OK;
+  const kda::LinaDecodeArgs a{q,    k,    v,  g,    per_head != 0, state, o, (int64_t)s.B * s.H,
+                              ntok, s.H, Hk, s.dk, s.dv,          s.dtype == KDA_BF16, stream};
+  return kda::launch_lina_decode(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_lina_chunk_fwd_workspace_size(const kda_shape* shape) {
+  int es = 0;
+  return check_lina_shape(shape, 1, false, -1, &es) == KDA_OK ? fwd_layout(*shape, -1).bytes : 0;
+}
+
+int kda_lina_chunk_fwd(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                       const float* log_decay, int decay_per_head, const float* initial_state, void* o,
+                       float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+  return fwd_impl(shape, qk_heads, nullptr, -1, q, k, v, log_decay, decay_per_head, initial_state, o, final_state,
+                  workspace, workspace_bytes, stream);
+}
+
+size_t kda_lina_chunk_fwd_varlen_workspace_size(const kda_shape* shape, int n_seqs) {
+  int es = 0;
+  return n_seqs >= 0 && check_lina_shape(shape, 1, false, n_seqs, &es) == KDA_OK ? fwd_layout(*shape, n_seqs).bytes : 0;
+}
+
+int kda_lina_chunk_fwd_varlen(const kda_shape* shape, int qk_heads, const int* cu_seqlens, int n_seqs, const void* q,
+                              const void* k, const void* v, const float* log_decay, int decay_per_head,
+                              const float* initial_state, void* o, float* final_state, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!shape) return KDA_ERR_NULL;
+  if (n_seqs < 0) return KDA_ERR_SHAPE;
+  return fwd_impl(shape, qk_heads, cu_seqlens, n_seqs, q, k, v, log_decay, decay_per_head, initial_state, o,
+                  final_state, workspace, workspace_bytes, stream);
+}
+
+size_t kda_lina_chunk_bwd_workspace_size(const kda_shape* shape, int qk_heads) {
+  int es = 0;
+  return check_lina_shape(shape, qk_heads, false, -1, &es) == KDA_OK ? bwd_layout(*shape, qk_heads, -1).bytes : 0;
+}
+
+int kda_lina_chunk_bwd(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                       const float* log_decay, int decay_per_head, const float* initial_state, const void* d_o,
+                       const float* d_final_state, void* dq, void* dk, void* dv, float* d_log_decay,
+                       float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
+  const BwdPtrs p{q,  k,  v,  log_decay,   decay_per_head,  initial_state, d_o, d_final_state,
+                  dq, dk, dv, d_log_decay, d_initial_state, workspace,     workspace_bytes};
+  return bwd_impl(shape, qk_heads, nullptr, -1, p, stream);
+}
+
+size_t kda_lina_chunk_bwd_varlen_workspace_size(const kda_shape* shape, int qk_heads, int n_seqs) {
+  int es = 0;
+  return n_seqs >= 0 && check_lina_shape(shape, qk_heads, false, n_seqs, &es) == KDA_OK
+             ? bwd_layout(*shape, qk_heads, n_seqs).bytes
+             : 0;
+}
+
+int kda_lina_chunk_bwd_varlen(const kda_shape* shape, int qk_heads, const int* cu_seqlens, int n_seqs, const void* q,
+                              const void* k, const void* v, const float* log_decay, int decay_per_head,
+                              const float* initial_state, const void* d_o, const float* d_final_state, void* dq,
+                              void* dk, void* dv, float* d_log_decay, float* d_initial_state, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!shape) return KDA_ERR_NULL;
+  if (n_seqs < 0) return KDA_ERR_SHAPE;
+  const BwdPtrs p{q,  k,  v,  log_decay,   decay_per_head,  initial_state, d_o, d_final_state,
+                  dq, dk, dv, d_log_decay, d_initial_state, workspace,     workspace_bytes};
+  return bwd_impl(shape, qk_heads, cu_seqlens, n_seqs, p, stream);
+}
+
+int kda_lina_decode_step(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                         const float* log_decay, int decay_per_head, float* state, void* o, void* stream) {
+  return decode_impl(shape, qk_heads, 1, q, k, v, log_decay, decay_per_head, state, o, stream);
+}
+
+int kda_lina_decode_tokens(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                           const float* log_decay, int decay_per_head, float* state, void* o, void* stream) {
+  if (!shape) return KDA_ERR_NULL;
+  return decode_impl(shape, qk_heads, shape->T, q, k, v, log_decay, decay_per_head, state, o, stream);
+}
+
+}  // extern "C"

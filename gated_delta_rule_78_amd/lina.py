@@ -1,0 +1,180 @@
+"""Linear attention with a decay per head: binding of the ``kda_lina_*`` entry points.
+
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+
+The delta rule of the other entry points without its erase term, with one gate per head; the
+states have the same layout.  As everywhere here, nothing is normalised or scaled inside (see
+``qk_norm_rope`` for q and k) and there is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import gated_delta_rule_78_amd as _kda
+
+
+def _operands(q, k, v, log_decay, lead):
+    """Checks shared by every form; lead: the shape before the heads.  Returns (Hk, H, dk, dv, code, per_head)."""
+    torch = _kda._torch()
+    n = len(lead)
+    if q.dim() != n + 2 or v.dim() != n + 2:
+        raise ValueError(f"q, k, v have {n + 2} dimensions")
+    Hk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    code = _kda._dtype_code(q)
+    for t, nm in ((k, "k"), (v, "v")):
+        if t.dtype != q.dtype:
+            raise TypeError(f"{nm} must have the dtype of q")
+    if k.shape != q.shape or v.shape != (*lead, H, dv) or Hk < 1 or H % max(Hk, 1) != 0:
+        raise ValueError("shapes: q, k [..., Hk, dk]; v [..., H, dv] with H a multiple of Hk")
+    if log_decay.dtype != torch.float32:
+        raise TypeError("log_decay must be float32")
+    per_head = log_decay.dim() == 1
+    if log_decay.shape != ((H,) if per_head else (*lead, H)):
+        raise ValueError("log_decay: [..., H] as v, or [H]")
+    return Hk, H, dk, dv, code, per_head
+
+
+def _states(ts, n, H, dk, dv):
+    torch = _kda._torch()
+    for t, nm in ts:
+        if t is not None and (t.dtype != torch.float32 or t.shape != (n, H, dk, dv)):
+            raise ValueError(f"{nm} must be float32 [{n},{H},{dk},{dv}]")
+
+
+def _packed(cu_seqlens, B):
+    torch = _kda._torch()
+    if cu_seqlens is None:
+        return B
+    if B != 1:
+        raise ValueError("a packed batch has B == 1")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise TypeError("cu_seqlens must be a 1-D int32 tensor")
+    return cu_seqlens.numel() - 1
+
+
+def _workspace(need, workspace, dev):
+    torch = _kda._torch()
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    return workspace, ctypes.c_size_t(workspace.numel() * workspace.element_size())
+
+
+def lina_chunk_fwd(q, k, v, log_decay, initial_state=None, out=None, final_state=None, want_final=True,
+                   cu_seqlens=None, workspace=None):
+    """Chunked forward over whole sequences.  q, k [B,T,Hk,dk] and v [B,T,H,dv] (all bf16 or all
+    fp32, contiguous; Hk divides H, head h of v goes with head h // (H // Hk) of q and k);
+    log_decay fp32 [B,T,H], or [H] for a fixed decay per head; initial_state fp32 [B,H,dk,dv] or
+    None.  cu_seqlens (int32 [N+1] on the device): a packed batch, B == 1, states [N,H,dk,dv];
+    tokens after the last offset are not written.  Returns (o [B,T,H,dv], final_state fp32 or
+    None)."""
+    torch = _kda._torch()
+    B, T = q.shape[:2]
+    Hk, H, dk, dv, code, per_head = _operands(q, k, v, log_decay, (B, T))
+    n = _packed(cu_seqlens, B)
+    dev = q.device
+    if out is None:
+        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.shape != (B, T, H, dv):
+        raise ValueError("out must be [B,T,H,dv] in the dtype of q")
+    if final_state is None and want_final:
+        final_state = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
+    _states(((initial_state, "initial_state"), (final_state, "final_state")), n, H, dk, dv)
+    shape = _kda.Shape(B, T, H, dk, dv, 64, code)
+    L = _kda.lib()
+    if cu_seqlens is None:
+        need = int(L.kda_lina_chunk_fwd_workspace_size(ctypes.byref(shape)))
+    else:
+        need = int(L.kda_lina_chunk_fwd_varlen_workspace_size(ctypes.byref(shape), n))
+    workspace, nbytes = _workspace(need, workspace, dev)
+    p = _kda._ptr
+    _kda._check((q, k, v, log_decay, cu_seqlens, initial_state, out, final_state, workspace),
+                ("q", "k", "v", "log_decay", "cu_seqlens", "initial_state", "out", "final_state", "workspace"), dev)
+    args = (p(q), p(k), p(v), p(log_decay), int(per_head), p(initial_state), p(out), p(final_state), p(workspace),
+            nbytes, _kda._stream(dev))
+    with torch.cuda.device(dev):
+        if cu_seqlens is None:
+            rc, where = L.kda_lina_chunk_fwd(ctypes.byref(shape), Hk, *args), "kda_lina_chunk_fwd"
+        else:
+            rc = L.kda_lina_chunk_fwd_varlen(ctypes.byref(shape), Hk, p(cu_seqlens), n, *args)
+            where = "kda_lina_chunk_fwd_varlen"
+    if rc != 0:
+        raise _kda.KdaError(rc, where)
+    return out, final_state
+
+
+def lina_chunk_bwd(q, k, v, log_decay, d_o, initial_state=None, d_final_state=None, want_d_decay=True,
+                   want_d_initial=True, cu_seqlens=None, workspace=None):
+    """Gradients of L = sum <d_o, o> + <d_final_state, S_T> through lina_chunk_fwd, which is
+    recomputed inside.  Inputs as lina_chunk_fwd; d_o [B,T,H,dv] in the dtype of q;
+    d_final_state fp32 [B or N,H,dk,dv] or None (zeros).  Returns (dq, dk, dv, d_log_decay or
+    None, d_initial_state or None): dq, dk, dv in the shape and dtype of q, k, v (shared heads
+    get the sum), d_log_decay fp32 in the shape of log_decay, d_initial_state fp32.  Tokens of a
+    packed batch after the last offset get zeros."""
+    torch = _kda._torch()
+    B, T = q.shape[:2]
+    Hk, H, dk, dv, code, per_head = _operands(q, k, v, log_decay, (B, T))
+    if d_o.dtype != q.dtype or d_o.shape != v.shape:
+        raise ValueError("d_o must be [B,T,H,dv] in the dtype of q")
+    n = _packed(cu_seqlens, B)
+    _states(((initial_state, "initial_state"), (d_final_state, "d_final_state")), n, H, dk, dv)
+    dev = q.device
+    new = torch.zeros_like if cu_seqlens is not None else torch.empty_like
+    gq, gk, gv = new(q), new(k), new(v)
+    gd = new(log_decay) if want_d_decay else None
+    gs = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev) if want_d_initial else None
+    shape = _kda.Shape(B, T, H, dk, dv, 64, code)
+    L = _kda.lib()
+    if cu_seqlens is None:
+        need = int(L.kda_lina_chunk_bwd_workspace_size(ctypes.byref(shape), Hk))
+    else:
+        need = int(L.kda_lina_chunk_bwd_varlen_workspace_size(ctypes.byref(shape), Hk, n))
+    workspace, nbytes = _workspace(need, workspace, dev)
+    p = _kda._ptr
+    _kda._check((q, k, v, log_decay, d_o, cu_seqlens, initial_state, d_final_state, workspace),
+                ("q", "k", "v", "log_decay", "d_o", "cu_seqlens", "initial_state", "d_final_state", "workspace"), dev)
+    args = (p(q), p(k), p(v), p(log_decay), int(per_head), p(initial_state), p(d_o), p(d_final_state), p(gq), p(gk),
+            p(gv), p(gd), p(gs), p(workspace), nbytes, _kda._stream(dev))
+    with torch.cuda.device(dev):
+        if cu_seqlens is None:
+            rc, where = L.kda_lina_chunk_bwd(ctypes.byref(shape), Hk, *args), "kda_lina_chunk_bwd"
+        else:
+            rc = L.kda_lina_chunk_bwd_varlen(ctypes.byref(shape), Hk, p(cu_seqlens), n, *args)
+            where = "kda_lina_chunk_bwd_varlen"
+    if rc != 0:
+        raise _kda.KdaError(rc, where)
+    return gq, gk, gv, gd, gs
+
+
+def _decode(entry, q, k, v, log_decay, state, out, lead):
+    torch = _kda._torch()
+    Hk, H, dk, dv, code, per_head = _operands(q, k, v, log_decay, lead)
+    B, T = lead[0], lead[1] if len(lead) > 1 else 1
+    _states(((state, "state"),), B, H, dk, dv)
+    dev = q.device
+    if out is None:
+        out = torch.empty_like(v)
+    elif out.dtype != q.dtype or out.shape != v.shape:
+        raise ValueError("out must have the shape of v and the dtype of q")
+    p = _kda._ptr
+    _kda._check((q, k, v, log_decay, state, out), ("q", "k", "v", "log_decay", "state", "out"), dev)
+    shape = _kda.Shape(B, T, H, dk, dv, 0, code)
+    with torch.cuda.device(dev):
+        rc = getattr(_kda.lib(), entry)(ctypes.byref(shape), Hk, p(q), p(k), p(v), p(log_decay), int(per_head),
+                                        p(state), p(out), _kda._stream(dev))
+    if rc != 0:
+        raise _kda.KdaError(rc, entry)
+    return out
+
+
+def lina_decode_step(q, k, v, log_decay, state, out=None):
+    """One recurrent token for every (b, h): q, k [B,Hk,dk]; v [B,H,dv]; log_decay fp32 [B,H] or
+    [H]; state fp32 [B,H,dk,dv] updated in place.  Returns o [B,H,dv]."""
+    return _decode("kda_lina_decode_step", q, k, v, log_decay, state, out, tuple(q.shape[:1]))
+
+
+def lina_decode_tokens(q, k, v, log_decay, state, out=None):
+    """Several tokens per (b, h) with the state read and written once: q, k [B,T,Hk,dk];
+    v [B,T,H,dv]; log_decay fp32 [B,T,H] or [H]; state fp32 [B,H,dk,dv] in place.
+    Returns o [B,T,H,dv]."""
+    return _decode("kda_lina_decode_tokens", q, k, v, log_decay, state, out, tuple(q.shape[:2]))

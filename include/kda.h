@@ -29,7 +29,8 @@
  *                      with its workspace query further down.
  * Variants further down: the two-pass forward with a caller workspace, packed
  * variable-length batches, multi-token decode, Gated DeltaNet-2 gates and SFDA
- * complex gates, each with its backward.
+ * complex gates, each with its backward; linear attention with a decay per head
+ * (kda_lina_*); the norm and position rotation of q and k (kda_qk_norm_rope).
  *
  * Conventions shared by all entry points
  *   - Every pointer except `shape` is a DEVICE pointer on the current HIP
@@ -424,6 +425,139 @@ int kda_decode_tokens(const kda_shape* shape, const void* q, const void* k, cons
 int kda_gdn2_decode_tokens(const kda_shape* shape, const void* q, const void* k, const void* v,
                            const void* alpha, const void* erase_gate, const void* write_gate,
                            float* state, void* o, void* stream);
+
+/*
+ * Linear attention with a decay per head: the recurrence above without its erase term and
+ * with one gate for all channels of a head,
+ *   S_t = e^(g_t) S_(t-1) + k_t v_t^T ,   o_t = S_t^T q_t ,
+ * chunked for whole sequences, recurrent for single tokens.  States have the layout of the
+ * other entry points.
+ *   qk_heads       : heads of q and k, a divisor of shape->H (KDA_ERR_SHAPE otherwise); head h
+ *                    of v, o, the decays and the states goes with q / k head
+ *                    h / (shape->H / qk_heads).
+ *   q, k           : [B, T, qk_heads, dk], v, o : [B, T, H, dv], in shape->dtype (both dtypes
+ *                    with every dk, dv in {64, 128})
+ *   log_decay      : fp32 natural logarithms g, [B, T, H], or [H] when decay_per_head is not
+ *                    zero.  g <= 0 is the intended range (not checked); -inf forgets the
+ *                    state exactly.
+ *   initial_state  : [B, H, dk, dv] fp32, or NULL for zeros
+ *   final_state    : [B, H, dk, dv] fp32, or NULL (not written); may equal initial_state
+ *   workspace      : kda_lina_chunk_fwd_workspace_size(shape) bytes, 256-byte aligned (0 bytes,
+ *                    and NULL accepted, when the chains are walked whole; with fewer chains
+ *                    than compute units it holds the end states of their segments)
+ * Arithmetic: fp32 sums, decays and states; with bf16 inputs the products r o q.k and the state
+ * as q meets it are rounded to bf16 (as o is), what is added to the state is not (2^-17).
+ * A non-finite v_t reaches the outputs from token t on only.  Alignment: 16 bytes for q, k, v,
+ * o and the states, 4 for log_decay.  Aliasing, packed batches (cu_seqlens, n_seqs, states of
+ * [n_seqs, H, dk, dv], token rows after the last offset not written) and errors as
+ * kda_chunk_fwd_ws and kda_chunk_fwd_varlen.  H <= 65535.
+ */
+size_t kda_lina_chunk_fwd_workspace_size(const kda_shape* shape); /* 0 also if the shape is invalid */
+int kda_lina_chunk_fwd(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                       const float* log_decay, int decay_per_head, const float* initial_state, void* o,
+                       float* final_state, void* workspace, size_t workspace_bytes, void* stream);
+size_t kda_lina_chunk_fwd_varlen_workspace_size(const kda_shape* shape, int n_seqs);
+int kda_lina_chunk_fwd_varlen(const kda_shape* shape, int qk_heads, const int* cu_seqlens, int n_seqs, const void* q,
+                              const void* k, const void* v, const float* log_decay, int decay_per_head,
+                              const float* initial_state, void* o, float* final_state, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of kda_lina_chunk_fwd(_varlen): the gradients of
+ *   L = sum_t <d_o_t, o_t> + <d_final_state, S_T> .
+ *   d_o                 : [B, T, H, dv], dtype of q;  d_final_state : fp32 or NULL (zeros)
+ *   dq, dk, dv          : outputs in the layout and dtype of q, k, v (sums are fp32 and rounded
+ *                         once; q / k heads that serve several heads get the sum over them)
+ *   d_log_decay         : fp32, layout of log_decay ([H]: summed over batch and tokens), or
+ *                         NULL when not wanted.  At g = -inf it is 0, as e^g is.
+ *   d_initial_state     : fp32, or NULL when not wanted
+ *   workspace           : the size below, 256-byte aligned
+ * Token rows after the last offset of a packed batch are not written.  No output may overlap
+ * an input, another output or the workspace (KDA_ERR_ALIAS).  Results do not depend on timing:
+ * every sum has a fixed order.
+ */
+size_t kda_lina_chunk_bwd_workspace_size(const kda_shape* shape, int qk_heads); /* 0 if invalid */
+int kda_lina_chunk_bwd(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                       const float* log_decay, int decay_per_head, const float* initial_state, const void* d_o,
+                       const float* d_final_state, void* dq, void* dk, void* dv, float* d_log_decay,
+                       float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+size_t kda_lina_chunk_bwd_varlen_workspace_size(const kda_shape* shape, int qk_heads, int n_seqs);
+int kda_lina_chunk_bwd_varlen(const kda_shape* shape, int qk_heads, const int* cu_seqlens, int n_seqs, const void* q,
+                              const void* k, const void* v, const float* log_decay, int decay_per_head,
+                              const float* initial_state, const void* d_o, const float* d_final_state, void* dq,
+                              void* dk, void* dv, float* d_log_decay, float* d_initial_state, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * The recurrent form: one token (q, k [B, qk_heads, dk]; v, o [B, H, dv]; log_decay [B, H] or
+ * [H]), or shape->T tokens in order ([B, T, ...]), for every (b, h), the fp32 state
+ * [B, H, dk, dv] read once and updated in place.  Rules as kda_decode_step and
+ * kda_decode_tokens (16-byte aligned state, element alignment otherwise).
+ */
+int kda_lina_decode_step(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                         const float* log_decay, int decay_per_head, float* state, void* o, void* stream);
+int kda_lina_decode_tokens(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                           const float* log_decay, int decay_per_head, float* state, void* o, void* stream);
+
+/*
+ * Queries and keys as the entry points above take them: each head's norm and the rotation by
+ * the token's position, in one pass,
+ *   y = R(theta) (w + weight_offset) o x r ,
+ *   r = (mean_c x_c^2 + eps)^(-1/2) (KDA_NORM_RMS), (sum_c x_c^2 + eps)^(-1/2) (KDA_NORM_L2: the
+ *       unit k of the delta rule) or 1 (KDA_NORM_NONE);  w = 1 - weight_offset where no weight
+ *       is given,
+ *   R turns the channel pairs (c, c + rotary_dim / 2), or (2c, 2c + 1) when interleaved, by
+ *   theta_c = positions[axis(c)] inv_freq[c], c < rotary_dim / 2; channels from rotary_dim on
+ *   are not turned.  (Turning q and k by t theta is what SFDA's gates e^(i theta) do inside the
+ *   recurrence, with the state in turned coordinates.)
+ *   q : [tokens, q_heads, d], k : [tokens, k_heads, d] in dtype, d 64 or 128; rows of a token
+ *       dense, tokens q_stride / k_stride elements apart (a multiple of 16 bytes; 0 = dense):
+ *       both may lie in one projection's output.  k_heads 0: no keys, k NULL.
+ *   q_weight, k_weight : [d] fp32, or NULL
+ *   inv_freq  : [rotary_dim / 2] DOUBLE (angles are formed in 64 bits: an fp32 product is
+ *               0.03 radians off at position 10^6);  NULL when rotary_dim is 0
+ *   positions : [n_axes, tokens] int32, or int64 when positions_64;  NULL when rotary_dim is 0.
+ *               With several axes (time, height, width) the first sections[0] frequencies turn
+ *               with axis 0, the next sections[1] with axis 1, and so on (their sum is
+ *               rotary_dim / 2, KDA_ERR_SHAPE otherwise).
+ *   q_out, k_out : dense; may equal dense q / k (in place), any other overlap is KDA_ERR_ALIAS
+ * rotary_dim: 0 or a multiple of 16, n_axes 1 to 4 (KDA_ERR_UNSUPPORTED otherwise).  q, k and
+ * the outputs are 16-byte aligned.  Sums, angles and weights are fp32 or wider, the result is
+ * rounded once.  A row of zeros with eps = 0 gives NaN, as the formula does.
+ */
+typedef enum { KDA_NORM_NONE = 0, KDA_NORM_RMS = 1, KDA_NORM_L2 = 2 } kda_norm;
+
+typedef struct {
+    long long tokens;   /* B * T, >= 0 */
+    int q_heads, k_heads;
+    int d;
+    long long q_stride, k_stride;
+    int norm;           /* kda_norm */
+    float eps;          /* >= 0 */
+    float weight_offset;
+    int rotary_dim;
+    int interleaved;
+    int n_axes;
+    int sections[4];
+    int positions_64;
+    kda_dtype dtype;
+} kda_qk_shape;
+
+int kda_qk_norm_rope(const kda_qk_shape* shape, const void* q, const void* k, const float* q_weight,
+                     const float* k_weight, const double* inv_freq, const void* positions, void* q_out, void* k_out,
+                     void* stream);
+
+/*
+ * Its gradients: d_q_out, d_k_out dense in dtype; dq, dk dense in dtype (each may equal its
+ * d_*_out, or dense q / k); d_q_weight, d_k_weight [d] fp32, summed over tokens and heads in a
+ * fixed order, or NULL when not wanted (KDA_ERR_NULL when wanted without the weight).
+ * workspace: the size below, 256-byte aligned, needed only with a weight gradient.
+ */
+size_t kda_qk_norm_rope_bwd_workspace_size(const kda_qk_shape* shape); /* 0 if invalid */
+int kda_qk_norm_rope_bwd(const kda_qk_shape* shape, const void* d_q_out, const void* d_k_out, const void* q,
+                         const void* k, const float* q_weight, const float* k_weight, const double* inv_freq,
+                         const void* positions, void* dq, void* dk, float* d_q_weight, float* d_k_weight,
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable text for a kda_status value (static storage). */
 const char* kda_status_string(int status);
