@@ -125,6 +125,54 @@ __device__ __forceinline__ void ld_quad<float>(const void* p, size_t i, float (&
   x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
 }
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// One chunk's rows of an operand as a buffer of the rows that exist: what lies behind them
+// reads as zeros and is not written, without a branch.
+struct Rows {
+#ifndef KDA_HOST_PASS
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Rows(const void* p, uint32_t bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000)) {}
+  __device__ __forceinline__ u32x4_t load16(uint32_t off) const {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  }
+  __device__ __forceinline__ u32x2_t load8(uint32_t off) const {
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+  }
+  __device__ __forceinline__ void store16(uint32_t off, u32x4_t x) const {
+    __builtin_amdgcn_raw_buffer_store_b128(x, r, off, 0, 0);
+  }
+  __device__ __forceinline__ void store8(uint32_t off, u32x2_t x) const {
+    __builtin_amdgcn_raw_buffer_store_b64(x, r, off, 0, 0);
+  }
+#else
+  __device__ Rows(const void*, uint32_t) {}
+  __device__ u32x4_t load16(uint32_t) const { return u32x4_t{}; }
+  __device__ u32x2_t load8(uint32_t) const { return u32x2_t{}; }
+  __device__ void store16(uint32_t, u32x4_t) const {}
+  __device__ void store8(uint32_t, u32x2_t) const {}
+#endif
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {  // results under 2^-126 are zero
+#ifndef KDA_HOST_PASS
+  return __builtin_amdgcn_exp2f(x);
+#else
+  return x;
+#endif
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+#ifndef KDA_HOST_PASS
+  const uint32_t a = __builtin_amdgcn_readfirstlane((uint32_t)x), b = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (int64_t)(((uint64_t)b << 32) | a);
+#else
+  return x;
+#endif
+}
+
 // sum over the 16 lanes of a DPP row, in every lane
 __device__ __forceinline__ float row16_sum(float x) {
 #define KDA_ROR(n) x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + n, 0xF, 0xF, true))
@@ -174,9 +222,9 @@ __device__ __forceinline__ void chunk_decays(Decays& d, float gr, int lane) {
   const float hi = rintf((float)s * 8.f) * 0.125f;
   d.hi[lane] = hi;
   d.lo[lane] = (float)(s - (double)hi);
-  d.row[lane] = exp2f((float)s);
-  d.col[lane] = exp2f((float)(tot - s));
-  if (lane == 0) d.tot = exp2f((float)tot);
+  d.row[lane] = fast_exp2((float)s);
+  d.col[lane] = fast_exp2((float)(tot - s));
+  if (lane == 0) d.tot = fast_exp2((float)tot);
 }
 
 struct WalkParams {
@@ -188,7 +236,7 @@ struct WalkParams {
 
 // STATE_ONLY: end states of the segments from a zero start, nothing else
 template <typename T, int DK, bool REV, int DOT, bool STATE_ONLY>
-__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(const WalkParams p) {
+__global__ __launch_bounds__(NT, sizeof(T) == 2 && (DOT == kDotNone || DK == 64) ? 2 : 1) void lina_walk_kernel(const WalkParams p) {
   constexpr int KS = DK / 32;   // product steps over the channels
   constexpr int CT = DK / 16;   // state tiles of a wave
   constexpr int QU = C * DK * (int)sizeof(T) / 16 / NT;  // 16-byte units a thread stages of Q or K
@@ -246,6 +294,8 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
     lo = (int64_t)sq * w.T;
     hi = lo + w.T;
   }
+  lo = uniform64(lo);
+  hi = uniform64(hi);
   const int nch = (int)((hi - lo + C - 1) / C);
   const int nsg = nch > 0 ? (nch + w.L - 1) / w.L : 1;
   if (sg >= nsg) return;
@@ -265,35 +315,69 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
   const char* gk = base(w.k, DK);
   const char* gv = base(w.v, w.dv) + (size_t)vt * VT * sizeof(T);
   const char* gx = DOT != kDotNone ? base(w.x, w.dv) + (size_t)vt * VT * sizeof(T) : nullptr;
-  const size_t rq = (size_t)w.q.heads * DK * sizeof(T), rk = (size_t)w.k.heads * DK * sizeof(T);
-  const size_t rv = (size_t)w.v.heads * w.dv * sizeof(T), rx = (size_t)w.x.heads * w.dv * sizeof(T);
+  const uint32_t rq = w.q.heads * DK * (uint32_t)sizeof(T), rk = w.k.heads * DK * (uint32_t)sizeof(T);
+  const uint32_t ro = w.H * w.dv;  // elements between two tokens of the output
+  const uint32_t rv = w.v.heads * w.dv * (uint32_t)sizeof(T), rx = w.x.heads * w.dv * (uint32_t)sizeof(T);
 
   // token of row r of chunk c (reverse walks count rows from the chunk's last token)
   auto token = [&](int c, int r) { return lo + (int64_t)c * C + (REV ? C - 1 - r : r); };
 
-  uint4 rgq[QU], rgk[QU], rgv[VU], rgx[DOT == kDotCross ? VU : 1];
-  float rgg = 0.f;
+  // tiles of the next chunk in registers; off*: a thread's bytes from the chunk's first token
+  u32x4_t rgq[STATE_ONLY ? 1 : QU], rgk[QU], rgv[VU], rgx[DOT == kDotCross ? VU : 1];
+  u32x4_t rgd[DOT == kDotRow ? 4 : 1];  // kDotRow: four columns of X for each token tile (bf16: in .xy)
+  auto tile_row = [&](int r) { return (uint32_t)(REV ? C - 1 - r : r); };
   auto prefetch = [&](int c) {
-    const uint4 z = make_uint4(0, 0, 0, 0);
+    const int64_t t0 = lo + (int64_t)c * C;
+    const uint32_t have = (uint32_t)min((int64_t)C, hi - t0);
+    const Rows bk(gk + (size_t)t0 * rk, have * rk), bv(gv + (size_t)t0 * rv, have * rv);
 #pragma unroll
     for (int i = 0; i < QU; ++i) {
-      const int u = tid + NT * i, r = u / (KT::RB / 16), x = u % (KT::RB / 16);
-      const int64_t t = token(c, r);
-      const bool in = t < hi;
-      if (!STATE_ONLY) rgq[i] = in ? *(const uint4*)(gq + (size_t)t * rq + 16 * x) : z;
-      rgk[i] = in ? *(const uint4*)(gk + (size_t)t * rk + 16 * x) : z;
+      const int u = tid + NT * i;
+      rgk[i] = bk.load16(tile_row(u / (KT::RB / 16)) * rk + u % (KT::RB / 16) * 16);
     }
 #pragma unroll
     for (int i = 0; i < VU; ++i) {
-      const int u = tid + NT * i, r = u / (VTl::RB / 16), x = u % (VTl::RB / 16);
-      const int64_t t = token(c, r);
-      const bool in = t < hi;
-      rgv[i] = in ? *(const uint4*)(gv + (size_t)t * rv + 16 * x) : z;
-      if (DOT == kDotCross && !STATE_ONLY) rgx[i] = in ? *(const uint4*)(gx + (size_t)t * rx + 16 * x) : z;
+      const int u = tid + NT * i;
+      rgv[i] = bv.load16(tile_row(u / (VTl::RB / 16)) * rv + u % (VTl::RB / 16) * 16);
     }
+    if constexpr (!STATE_ONLY) {
+      const Rows bq(gq + (size_t)t0 * rq, have * rq);
+#pragma unroll
+      for (int i = 0; i < QU; ++i) {
+        const int u = tid + NT * i;
+        rgq[i] = bq.load16(tile_row(u / (KT::RB / 16)) * rq + u % (KT::RB / 16) * 16);
+      }
+    }
+    if constexpr (DOT == kDotCross && !STATE_ONLY) {
+      const Rows bx(gx + (size_t)t0 * rx, have * rx);
+#pragma unroll
+      for (int i = 0; i < VU; ++i) {
+        const int u = tid + NT * i;
+        rgx[i] = bx.load16(tile_row(u / (VTl::RB / 16)) * rx + u % (VTl::RB / 16) * 16);
+      }
+    }
+    if constexpr (DOT == kDotRow && !STATE_ONLY) {
+      const Rows bx(gx + (size_t)t0 * rx, have * rx);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t off = tile_row(16 * t + n) * rx + (16 * wave + 4 * g) * (uint32_t)sizeof(T);
+        if constexpr (sizeof(T) == 2) {
+          const u32x2_t x = bx.load8(off);
+          rgd[t][0] = x[0];
+          rgd[t][1] = x[1];
+        } else {
+          rgd[t] = bx.load16(off);
+        }
+      }
+    }
+  };
+  // the decays run one chunk further ahead: loads return in order, and waiting for one issued
+  // after the tiles would wait for the tiles
+  float rgg = 0.f;
+  auto load_decay = [&](int c) {
     if (wave == 0) {
       const int64_t t = token(c, lane) + (REV ? 1 : 0);
-      rgg = t < hi ? (w.g_fixed ? w.g[h] : w.g[(size_t)t * w.H + h]) : 0.f;
+      rgg = c >= first && c < last && t < hi ? (w.g_fixed ? w.g[h] : w.g[(size_t)t * w.H + h]) : 0.f;
     }
   };
 
@@ -333,8 +417,10 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
 
   const int steps = last - first;
   if (steps > 0) {
-    prefetch(REV ? last - 1 : first);
+    load_decay(REV ? last - 1 : first);
     if (wave == 0) chunk_decays(dec[0], rgg, lane);
+    load_decay(REV ? last - 2 : first + 1);
+    prefetch(REV ? last - 1 : first);
   }
   for (int it = 0; it < steps; ++it) {
     const int c = REV ? last - 1 - it : first + it;
@@ -343,15 +429,26 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
 #pragma unroll
     for (int i = 0; i < QU; ++i) {
       const int u = tid + NT * i, r = u / (KT::RB / 16), x = u % (KT::RB / 16);
-      if (!STATE_ONLY) *(uint4*)(sQ + KT::unit(r, x)) = rgq[i];
-      *(uint4*)(sK + KT::unit(r, x)) = rgk[i];
+      if constexpr (!STATE_ONLY) *(u32x4_t*)(sQ + KT::unit(r, x)) = rgq[i];
+      *(u32x4_t*)(sK + KT::unit(r, x)) = rgk[i];
     }
 #pragma unroll
     for (int i = 0; i < VU; ++i) {
       const int u = tid + NT * i, r = u / (VTl::RB / 16), x = u % (VTl::RB / 16);
-      *(uint4*)(sV + VTl::unit(r, x)) = rgv[i];
-      if (DOT == kDotCross && !STATE_ONLY) *(uint4*)(sX + VTl::unit(r, x)) = rgx[i];
+      *(u32x4_t*)(sV + VTl::unit(r, x)) = rgv[i];
+      if constexpr (DOT == kDotCross && !STATE_ONLY) *(u32x4_t*)(sX + VTl::unit(r, x)) = rgx[i];
     }
+    float xd[DOT == kDotRow ? 4 : 1][4];
+    if constexpr (DOT == kDotRow && !STATE_ONLY) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          xd[t][i] = __uint_as_float(sizeof(T) == 4 ? rgd[t][i] : i & 1 ? rgd[t][i >> 1] & 0xFFFF0000u : rgd[t][i >> 1] << 16);
+    }
+    // the next chunk's decays (its logarithms arrived with this chunk's tiles)
+    if (wave == 0 && it + 1 < steps) chunk_decays(dec[(it + 1) & 1], rgg, lane);
+    load_decay(REV ? c - 2 : c + 2);
     if (it + 1 < steps) prefetch(REV ? c - 1 : c + 1);
     lds_barrier();
 
@@ -403,7 +500,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = 16 * J + 4 * g + i;
-              const float r = a[i] * exp2f((ih - jhs[i]) + (il - jls[i]));
+              const float r = a[i] * fast_exp2((ih - jhs[i]) + (il - jls[i]));
               x[i] = j <= row ? r : 0.f;
               if constexpr (DOT == kDotCross) {
                 const float m = j < row ? r * e[i] : 0.f;
@@ -451,9 +548,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
       if constexpr (DOT == kDotRow) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int64_t tk = token(c, 16 * t + n);
-          float x[4] = {0.f, 0.f, 0.f, 0.f};
-          if (tk < hi) ld_quad<T>(gx + (size_t)tk * rx, 16 * wave + 4 * g, x);
+          const float(&x)[4] = xd[t];
           float d = acc[t][0] * x[0] + acc[t][1] * x[1] + acc[t][2] * x[2] + acc[t][3] * x[3];
           d += __shfl_xor(d, 16);
           d += __shfl_xor(d, 32);
@@ -461,8 +556,6 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
         }
       }
     }
-    // the next chunk's decays, by the wave with the fewest tiles above
-    if (wave == 0 && it + 1 < steps) chunk_decays(dec[(it + 1) & 1], rgg, lane);
     if constexpr (!STATE_ONLY) lds_barrier();
 
     if constexpr (DOT != kDotNone && !STATE_ONLY) {
@@ -523,15 +616,20 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void lina_walk_kernel(c
           acc[t] = o;
         }
       }
+      const int64_t t0 = lo + (int64_t)c * C;
+      const uint32_t have = (uint32_t)min((int64_t)C, hi - t0);
+      if (sizeof(T) == 2 && !w.out_f32) {
+        const Rows bo((char*)w.out + ((size_t)t0 * w.H + h) * w.dv * 2 + vt * VT * 2, have * ro * 2);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int64_t tk = token(c, 16 * t + n);
-        if (tk < hi) {
-          const float x[4] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
-          const size_t at = ((size_t)tk * w.H + h) * w.dv + vt * VT + 16 * wave + 4 * g;
-          if (w.out_f32) st_quad<float>((char*)w.out + at * 4, x);
-          else st_quad<T>((char*)w.out + at * sizeof(T), x);
+        for (int t = 0; t < 4; ++t) {
+          const u32x2_t x = {pack_bf16x2(acc[t][0], acc[t][1]), pack_bf16x2(acc[t][2], acc[t][3])};
+          bo.store8((tile_row(16 * t + n) * ro + 16 * wave + 4 * g) * 2, x);
         }
+      } else {
+        const Rows bo((char*)w.out + ((size_t)t0 * w.H + h) * w.dv * 4 + vt * VT * 4, have * ro * 4);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          bo.store16((tile_row(16 * t + n) * ro + 16 * wave + 4 * g) * 4, __builtin_bit_cast(u32x4_t, acc[t]));
       }
     }
     // S <- decay S + K^T (col o V)
