@@ -29,7 +29,7 @@ struct LinaWalk {
   int dot = kDotNone;
   float* dots = nullptr;      // [dv / 64][H][rows] fp32
   float* snap = nullptr;      // states every kLinaGroup chunks (forward walk with kDotRow writes them)
-  float* anchor = nullptr;    // [groups][H][dv / 64] (reverse walk with kDotRow: <snap, state>)
+  float* anchor = nullptr;    // [groups][H][dv / 64][4] (reverse walk with kDotRow: <snap, state>)
   float* seg_state = nullptr; // [segments][H][dv / 64][dk * 64]
   float* seg_dec = nullptr;   // [segments][H]
   // batch

@@ -147,7 +147,7 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   l.off_cs = up(l.off_dec + seg * s.H * 4);
   l.off_snap = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
   l.off_anchor = up(l.off_snap + l.groups * state);
-  l.off_a = up(l.off_anchor + (size_t)l.groups * s.H * (s.dk / 64) * 4);
+  l.off_a = up(l.off_anchor + (size_t)l.groups * s.H * (s.dk / 64) * 4 * 4);
   const size_t dots = (size_t)toks * s.H * 4;
   l.off_b = up(l.off_a + dots * (s.dk / 64));
   l.off_e = up(l.off_b + dots * (s.dk / 64));
