@@ -38,8 +38,8 @@ namespace kda {
 namespace {
 
 // bf16: eight waves, two to a SIMD, one barrier per chunk.  Waves 0-3 keep the state and make
-// the outputs of chunk c; waves 4-7 meanwhile write the tiles of chunk c + 2 to LDS (fetched a
-// step before), compute its decays, and make P of chunk c + 1, so that neither the fetch nor
+// the outputs of chunk c; waves 4-7 meanwhile write the tiles of chunk c + 2 to LDS (fetched two
+// steps before, into the one of two register sets that is free), compute its decays, and make P of chunk c + 1, so that neither the fetch nor
 // Q K^T lies on the state's path.  Tiles are triple-, P double-buffered.
 template <int DK, int DOT>
 struct PipeLds {
@@ -73,58 +73,66 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
   if (threadIdx.x >= NT) {
     if (steps == 0) return;
     const Operand<T> q(w.q, w, ch.h, DK, 0), k(w.k, w, ch.h, DK, 0), v(w.v, w, ch.h, w.dv, ch.vt * VT);
-    Stage<T, DK> rq, rk;
-    Stage<T, VT> rv, rx;
-    auto fetch = [&](int it) {
+    struct Tiles {
+      Stage<T, DK> q, k;
+      Stage<T, VT> v, x;
+    } ra, rb;
+    auto fetch_to = [&](Tiles& r, int it) {
       const int c = chunk(it);
       const int64_t t = ch.lo + (int64_t)c * C;
       const uint32_t n = ch.rows(c);
-      rk.load(k.rows(t, n), k.step, REV, tid);
-      rq.load(q.rows(t, n), q.step, REV, tid);
-      rv.load(v.rows(t, n), v.step, REV, tid);
-      if constexpr (DOT == kDotCross) rx.load(x.rows(t, n), x.step, REV, tid);
+      r.k.load(k.rows(t, n), k.step, REV, tid);
+      r.q.load(q.rows(t, n), q.step, REV, tid);
+      r.v.load(v.rows(t, n), v.step, REV, tid);
+      if constexpr (DOT == kDotCross) r.x.load(x.rows(t, n), x.step, REV, tid);
     };
-    auto put = [&](int it) {
-      rk.store(tK(it), tid);
-      rq.store(tQ(it), tid);
-      rv.store(tV(it), tid);
-      if constexpr (DOT == kDotCross) rx.store(tX(it), tid);
+    auto put_from = [&](const Tiles& r, int it) {
+      r.k.store(tK(it), tid);
+      r.q.store(tQ(it), tid);
+      r.v.store(tV(it), tid);
+      if constexpr (DOT == kDotCross) r.x.store(tX(it), tid);
     };
-    // the decays' logarithms run a chunk ahead of the tiles: loads return in order, and waiting
-    // for one behind the tiles would wait for these
-    float rg = 0.f;
-    auto fetch_decay = [&](int it) {
-      if (wave == 0 && it < steps) rg = row_decay<REV>(w, ch, chunk(it), lane);
+    // wave 0's logarithms of the decays come with the tiles of their chunk, a step before these
+    // are written and two before they are used
+    float ga = 0.f, gb = 0.f;
+    auto fetch_decay = [&](float& g, int it) {
+      if (wave == 0) g = it < steps ? row_decay<REV>(w, ch, chunk(it), lane) : 0.f;
     };
-    auto decays = [&](int it) {
-      if (wave == 0 && it < steps) chunk_decays(dec[it % 3], rg, lane);
+    auto decays = [&](float g, int it) {
+      if (wave == 0 && it < steps) chunk_decays(dec[it % 3], g, lane);
     };
     auto scores = [&](int it) {
       make_p<T, DK, DOT>(tQ(it), tK(it), tV(it), tX(it), tP(it), dec[it % 3], sdot[DOT == kDotNone ? 0 : it & 1][wave],
                          sdot2[DOT == kDotCross ? it & 1 : 0], wave, lane);
     };
-    fetch_decay(0);
-    decays(0);
-    fetch_decay(1);
-    fetch(0);
-    decays(1);
-    fetch_decay(2);
-    put(0);
-    if (steps > 1) fetch(1);
+    fetch_decay(ga, 0);
+    fetch_to(ra, 0);
+    fetch_decay(gb, 1);
+    if (steps > 1) fetch_to(rb, 1);
+    decays(ga, 0);
+    put_from(ra, 0);
+    fetch_decay(ga, 2);
+    if (steps > 2) fetch_to(ra, 2);
+    decays(gb, 1);
     lds_barrier();
-    if (steps > 1) put(1);
-    if (steps > 2) fetch(2);
+    if (steps > 1) put_from(rb, 1);
+    fetch_decay(gb, 3);
+    if (steps > 3) fetch_to(rb, 3);
     scores(0);
     lds_barrier();
-    for (int it = 0; it < steps; ++it) {
-      if (it + 2 < steps) put(it + 2);
-      decays(it + 2);
-      fetch_decay(it + 3);
-      if (it + 3 < steps) fetch(it + 3);
+    auto step = [&](Tiles& r, float& g, int it) {
+      if (it + 2 < steps) put_from(r, it + 2);
+      decays(g, it + 2);
+      fetch_decay(g, it + 4);
+      if (it + 4 < steps) fetch_to(r, it + 4);
       if (it + 1 < steps) scores(it + 1);
       if constexpr (DOT == kDotRow)
         if (wave == 0 && it > 0) store_dots<DOT, REV>(p, ch, chunk(it - 1), sdot[(it - 1) & 1], sdot2[0], lane);
       lds_barrier();
+    };
+    for (int it = 0; it < steps; it += 2) {
+      step(ra, ga, it);
+      if (it + 1 < steps) step(rb, gb, it + 1);
     }
     if constexpr (DOT == kDotRow)
       if (wave == 0) store_dots<DOT, REV>(p, ch, chunk(steps - 1), sdot[(steps - 1) & 1], sdot2[0], lane);

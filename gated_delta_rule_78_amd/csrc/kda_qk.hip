@@ -279,19 +279,20 @@ __global__ __launch_bounds__(NT) void qk_bwd_kernel(const QkArgs a, int per) {
   }
 }
 
-// weight gradients: the blocks' parts in a fixed order, 64 channels by 16 threads each
+// weight gradients: the blocks' parts in a fixed order, 16 channels by 64 threads each (many
+// short columns in flight: with 64 channels by 16 threads this took 57 us at 2,048 blocks)
 __global__ __launch_bounds__(1024) void qk_dw_kernel(const float* __restrict__ partial, int blocks, int d,
                                                      float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ double s[16][64];
-  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + c;  // of 2 d
+  __shared__ double s[64][16];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int col = blockIdx.x * 16 + c;  // of 2 d
   double x = 0.;
-  for (int b = r; b < blocks; b += 16) x += partial[(size_t)b * 2 * d + col];
+#pragma unroll 8
+  for (int b = r; b < blocks; b += 64) x += partial[(size_t)b * 2 * d + col];
   s[r][c] = x;
   __syncthreads();
   if (r == 0) {
-#pragma unroll
-    for (int i = 1; i < 16; ++i) x += s[i][c];
+    for (int i = 1; i < 64; ++i) x += s[i][c];
     float* to = col < d ? dwq : dwk;
     if (to) to[col < d ? col : col - d] = (float)x;
   }
@@ -326,7 +327,7 @@ hipError_t bwd_t(const QkArgs& a) {
                      (hipStream_t)a.stream, a, per);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.partial) return e;
-  hipLaunchKernelGGL(qk_dw_kernel, dim3(2 * D / 64), dim3(1024), 0, (hipStream_t)a.stream, a.partial,
+  hipLaunchKernelGGL(qk_dw_kernel, dim3(2 * D / 16), dim3(1024), 0, (hipStream_t)a.stream, a.partial,
                      (int)(bx * parts), D, a.q.dw, a.k.dw);
   return hipGetLastError();
 }
