@@ -34,6 +34,7 @@ struct LinaWalk {
   float* seg_dec = nullptr;   // [segments][H]
   // batch
   const int* cs = nullptr;    // clamped offsets of a packed batch [n + 1], or NULL
+  const int* list = nullptr;  // its segments in the order they are dealt, [slots][2]
   int n = 0;                  // sequences
   int T = 0;                  // tokens of each sequence (packed: of the batch)
   int H = 0, dk = 0, dv = 0;  // the walk's own widths: Q, K have dk channels, V, out dv
@@ -50,7 +51,7 @@ constexpr int kLinaGroup = 16;  // chunks between two kept states of the backwar
 inline int64_t lina_pieces(int64_t rows, int64_t n, int64_t per) { return rows / (64 * per) + n; }
 
 hipError_t launch_lina_walk(const LinaWalk& w);
-hipError_t launch_lina_offsets(const int* cu, int n, int T, int* cs, void* stream);
+hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream);
 hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int heads, int group, int d, bool bf16,
                                void* stream);
 hipError_t launch_lina_ddecay(const LinaWalk& w, const float* a, const float* b, const float* e, int na, int ne,

@@ -261,12 +261,12 @@ __global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
   store_state<DK, REV>(p, ch, tid, S);
 }
 
-// End states of the segments from a zero start: the walk without its outputs.
+// End states of the segments from a zero start: the walk without its outputs.  Two tile
+// buffers, one barrier per chunk; small enough for three workgroups on a compute unit.
 template <typename T, int DK, bool REV, bool EXACT>
 __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
+  constexpr int TILES = Tile<T, DK>::BYTES + Tile<T, VT>::BYTES;
   extern __shared__ __align__(16) char smem[];
-  char* sK = smem;
-  char* sV = sK + Tile<T, DK>::BYTES;
   __shared__ Decays dec[2];
   const LinaWalk& w = p.w;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -275,42 +275,44 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
   const Operand<T> k(w.k, w, ch.h, DK, 0), v(w.v, w, ch.h, w.dv, ch.vt * VT);
   Stage<T, DK> rk;
   Stage<T, VT> rv;
-  auto fetch = [&](int c) {
+  float rg = 0.f;
+  const int steps = ch.last - ch.first;
+  auto chunk = [&](int it) { return REV ? ch.last - 1 - it : ch.first + it; };
+  auto fetch = [&](int it) {
+    if (it >= steps) return;
+    const int c = chunk(it);
     const int64_t t = ch.lo + (int64_t)c * C;
     const uint32_t n = ch.rows(c);
+    if (wave == 0) rg = row_decay<REV>(w, ch, c, lane);
     rk.load(k.rows(t, n), k.step, REV, tid);
     rv.load(v.rows(t, n), v.step, REV, tid);
   };
-  float rg = 0.f;
-  auto fetch_decay = [&](int c) {
-    if (wave == 0) rg = row_decay<REV>(w, ch, c, lane);
+  auto put = [&](int it) {
+    if (it >= steps) return;
+    char* t = smem + (it & 1) * TILES;
+    if (wave == 0) chunk_decays(dec[it & 1], rg, lane);
+    rk.store(t, tid);
+    rv.store(t + Tile<T, DK>::BYTES, tid);
   };
   f32x4_t S[DK / 16];
 #pragma unroll
   for (int ct = 0; ct < DK / 16; ++ct) S[ct] = zero4();
   float total = 1.f;
-  const int steps = ch.last - ch.first;
-  auto chunk = [&](int it) { return REV ? ch.last - 1 - it : ch.first + it; };
-  if (steps > 0) {
-    fetch_decay(chunk(0));
-    if (wave == 0) chunk_decays(dec[0], rg, lane);
-    fetch_decay(chunk(1));
-    fetch(chunk(0));
-  }
+  fetch(0);
+  put(0);
+  fetch(1);
+  lds_barrier();
   for (int it = 0; it < steps; ++it) {
+    put(it + 1);
+    fetch(it + 2);
     const Decays& dc = dec[it & 1];
-    lds_barrier();
-    rk.store(sK, tid);
-    rv.store(sV, tid);
-    if (wave == 0 && it + 1 < steps) chunk_decays(dec[(it + 1) & 1], rg, lane);
-    if (it + 2 < steps) fetch_decay(chunk(it + 2));
-    if (it + 1 < steps) fetch(chunk(it + 1));
-    lds_barrier();
+    const char* t = smem + (it & 1) * TILES;
     Frag<T> fv[2];
-    tok_frag<T, VT>(fv[0], sV, 16 * wave, 0, lane);
-    tok_frag<T, VT>(fv[1], sV, 16 * wave, 1, lane);
+    tok_frag<T, VT>(fv[0], t + Tile<T, DK>::BYTES, 16 * wave, 0, lane);
+    tok_frag<T, VT>(fv[1], t + Tile<T, DK>::BYTES, 16 * wave, 1, lane);
     total *= dc.tot;
-    add_chunk<T, DK, EXACT>(S, fv, sK, dc, lane);
+    add_chunk<T, DK, EXACT>(S, fv, t, dc, lane);
+    lds_barrier();
   }
   f32x4_t* to = (f32x4_t*)(w.seg_state + ch.at(p, ch.seg) * (DK * VT));
 #pragma unroll
@@ -359,7 +361,7 @@ hipError_t walk_f32(const WalkParams& p) {
 
 template <typename T, int DK>
 hipError_t segments(const WalkParams& p) {
-  const int lds = Tile<T, DK>::BYTES + Tile<T, VT>::BYTES;
+  const int lds = 2 * (Tile<T, DK>::BYTES + Tile<T, VT>::BYTES);
   const bool exact = sizeof(T) == 2 && p.w.dot == kDotRow;
   if (p.w.rev)
     return exact ? launch(lina_segment_kernel<T, DK, true, true>, p, NT, lds)
@@ -368,11 +370,15 @@ hipError_t segments(const WalkParams& p) {
                : launch(lina_segment_kernel<T, DK, false, false>, p, NT, lds);
 }
 
-// Packed offsets clamped to [0, T] and made non-decreasing (a running maximum), cs[0] = 0.
+// Packed offsets clamped to [0, T] and made non-decreasing (a running maximum), cs[0] = 0, and
+// the list of segments (sequence, segment), the longest first (in 64 classes): workgroups are
+// dealt in that order, so that no long chain starts last.  Order within a class is left to
+// chance; no result depends on it.  Slots that no segment needs hold -1.
 constexpr int NTB = 1024;
-__global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T,
-                                                           int* __restrict__ cs) {
-  __shared__ int part[NTB];
+__global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T, int L,
+                                                           int64_t slots, int* __restrict__ cs,
+                                                           int* __restrict__ list) {
+  __shared__ int part[NTB], from[64];
   const int tid = threadIdx.x, per = (nseq + NTB - 1) / NTB;
   const int s0 = min(nseq, tid * per), s1 = min(nseq, s0 + per);
   int mx = 0;
@@ -385,12 +391,49 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
     part[tid] = max(part[tid], v);
     __syncthreads();
   }
-  int run = tid ? part[tid - 1] : 0;
+  const int run0 = tid ? part[tid - 1] : 0;
+  if (tid < 64) from[tid] = 0;
   if (tid == 0) cs[0] = 0;
-  for (int i = s0; i < s1; ++i) {
-    run = max(run, min(max(cu[i + 1], 0), T));
-    cs[i + 1] = run;
+  __syncthreads();
+  auto each = [&](auto fn) {  // this thread's segments
+    int run = run0;
+    for (int i = s0; i < s1; ++i) {
+      const int end = max(run, min(max(cu[i + 1], 0), T));
+      const int nch = (end - run + C - 1) / C, nsg = nch > 0 ? (nch + L - 1) / L : 1;
+      fn(i, end, nch, nsg);
+      run = end;
+    }
+  };
+  auto cls = [&](int len) { return 63 - (int)((int64_t)len * 63 / L); };
+  each([&](int i, int end, int nch, int nsg) {
+    cs[i + 1] = end;
+    if (nsg > 1) atomicAdd(&from[0], nsg - 1);
+    atomicAdd(&from[cls(nch - (nsg - 1) * L)], 1);
+  });
+  __syncthreads();
+  if (tid == 0) {
+    int x = 0;
+    for (int i = 0; i < 64; ++i) {
+      const int n = from[i];
+      from[i] = x;
+      x += n;
+    }
+    part[0] = x;
   }
+  __syncthreads();
+  each([&](int i, int, int nch, int nsg) {
+    if (nsg > 1) {
+      const int at = atomicAdd(&from[0], nsg - 1);
+      for (int x = 0; x < nsg - 1; ++x) {
+        list[2 * (at + x)] = i;
+        list[2 * (at + x) + 1] = x;
+      }
+    }
+    const int at = atomicAdd(&from[cls(nch - (nsg - 1) * L)], 1);
+    list[2 * at] = i;
+    list[2 * at + 1] = nsg - 1;
+  });
+  for (int64_t x = part[0] + tid; x < slots; x += NTB) list[2 * x] = -1;
 }
 
 // dq, dk of heads that share them: [rows, H, d] fp32 -> [rows, heads, d], summed in order
@@ -515,8 +558,9 @@ hipError_t launch_lina_walk(const LinaWalk& w) {
   return w.dk == 128 ? walk_f32<128>(p) : walk_f32<64>(p);
 }
 
-hipError_t launch_lina_offsets(const int* cu, int n, int T, int* cs, void* stream) {
-  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, cs);
+hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream) {
+  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, L,
+                     lina_pieces(T, n, L), cs, list);
   return hipGetLastError();
 }
 

@@ -2,8 +2,10 @@
 // kda_lina_*): argument checks on the host, then the walks' launches.
 #include <stddef.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/kda.h"
 #include "kda_check.h"
@@ -28,15 +30,32 @@ int check_lina_shape(const kda_shape* s, int qk_heads, bool decode, int n_seqs, 
   return KDA_OK;
 }
 
-// Chunks of a segment.  A chain (sequence, head, 64 value columns) is walked in order; with
-// fewer chains than compute units it is cut into segments, whose start states cost one more
-// read of k and v.
 struct Plan {
-  int L;
+  int L;  // chunks of a segment
   bool split;
   int64_t nseg;
 };
 
+// KDA_LINA_SEGMENT=n pins the chunks of a segment (tuning aid, and the tests' forced splits).
+int segment_override() {
+  static const int v = [] {
+    const char* e = getenv("KDA_LINA_SEGMENT");
+    return e ? atoi(e) : 0;
+  }();
+  return v;
+}
+
+// A chain (sequence, head, 64 value columns) is walked in order; with fewer chains than compute
+// units it is cut into segments of L chunks, whose start states cost one more read of k and v
+// (the segments' end states first, then every segment from its own start).  Measured, bf16,
+// d = 128, forward: with 256 chains or more whole chains win; below, one segment per compute
+// unit (work / 256: 512 chunks of 8 chains 79 us at L = 16, 93 at 8, 96 at 24), or two where
+// segments stay long, for the sake of the first pass (128 chunks of 64 chains 131 us at L = 16,
+// 137 at 32, 245 whole; 2,048 of 32 chains 931 at 128, 991 at 256).  Short segments
+// cost their successors a state to add, nch / L of them in a row: with a step of s and an
+// addition of f, 2 L s + f nch / L is least at L = sqrt(nch f / 2 s) (64 chunks of 8 chains: 30 us
+// at L = 3, 53 at 1, 63 at 16; fp32, 16 chunks: 25 us at 1, 45 at 4, 107 whole).  Packed chains
+// are dealt longest first, and cut only where one alone would outlast the others.
 Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   const bool packed = n_seqs >= 0;
   const int64_t nch = std::max<int64_t>(1, ((int64_t)s.T + 63) / 64);
@@ -44,8 +63,13 @@ Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   const int64_t chains = std::max<int64_t>(1, n * s.H * nv);
   const int64_t work = (packed ? nch + n : nch * n) * s.H * nv;  // chunk steps in all
   int64_t L = nch;
-  if (packed || chains < 256) L = std::max<int64_t>(16, (work + 511) / 512);
-  L = std::min(L, nch);
+  if (packed || chains < 256) {
+    L = (work + 255) / 256;
+    if (!packed && L >= 32) L = (work + 511) / 512;
+    L = std::max<int64_t>(L, (int64_t)std::ceil(std::sqrt((double)nch * (s.dtype == KDA_BF16 ? 0.16 : 0.06))));
+  }
+  if (segment_override() > 0) L = segment_override();
+  L = std::max<int64_t>(1, std::min(L, nch));
   Plan p;
   p.L = (int)L;
   p.split = L < nch;
@@ -55,7 +79,7 @@ Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
 
 struct FwdLayout {
   Plan plan;
-  size_t off_dec, off_cs, bytes;
+  size_t off_dec, off_cs, off_list, bytes;
 };
 
 FwdLayout fwd_layout(const kda_shape& s, int n_seqs) {
@@ -64,7 +88,8 @@ FwdLayout fwd_layout(const kda_shape& s, int n_seqs) {
   const size_t seg = l.plan.split ? (size_t)l.plan.nseg : 0;
   l.off_dec = up(seg * s.H * s.dk * s.dv * 4);
   l.off_cs = up(l.off_dec + seg * s.H * 4);
-  l.bytes = n_seqs >= 0 ? up(l.off_cs + ((size_t)n_seqs + 1) * 4) : l.off_cs;
+  l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
+  l.bytes = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
   return l;
 }
 
@@ -123,7 +148,10 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
   a.stream = stream;
   if (packed) {
     a.cs = (const int*)(w + l.off_cs);
-    if (kda::launch_lina_offsets(cu, n_seqs, s.T, (int*)(w + l.off_cs), stream) != hipSuccess) return KDA_ERR_HIP;
+    a.list = (const int*)(w + l.off_list);
+    if (kda::launch_lina_offsets(cu, n_seqs, s.T, a.L, (int*)(w + l.off_cs), (int*)(w + l.off_list), stream) !=
+        hipSuccess)
+      return KDA_ERR_HIP;
   }
   return kda::launch_lina_walk(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
@@ -133,7 +161,7 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
 struct BwdLayout {
   Plan plan;
   int64_t groups;
-  size_t off_dec, off_cs, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
+  size_t off_dec, off_cs, off_list, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
 };
 
 BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
@@ -145,7 +173,8 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   l.groups = n_seqs >= 0 ? kda::lina_pieces(s.T, n, kda::kLinaGroup) : n * ((s.T + per - 1) / per);
   l.off_dec = up(seg * state);
   l.off_cs = up(l.off_dec + seg * s.H * 4);
-  l.off_snap = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
+  l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
+  l.off_snap = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
   l.off_anchor = up(l.off_snap + l.groups * state);
   l.off_a = up(l.off_anchor + (size_t)l.groups * s.H * (s.dk / 64) * 4 * 4);
   const size_t dots = (size_t)toks * s.H * 4;
@@ -223,7 +252,10 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
   }
   if (packed) {
     a.cs = (const int*)(ws + l.off_cs);
-    if (kda::launch_lina_offsets(cu, n_seqs, s.T, (int*)(ws + l.off_cs), stream) != hipSuccess) return KDA_ERR_HIP;
+    a.list = (const int*)(ws + l.off_list);
+    if (kda::launch_lina_offsets(cu, n_seqs, s.T, a.L, (int*)(ws + l.off_cs), (int*)(ws + l.off_list), stream) !=
+        hipSuccess)
+      return KDA_ERR_HIP;
   }
   const bool shared = s.H > Hk;
   float* share = (float*)(ws + l.off_share);

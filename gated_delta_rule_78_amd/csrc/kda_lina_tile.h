@@ -244,16 +244,12 @@ struct Chain {
     h = (int)(unit % hk) * (w.H / hk) + in / p.nv;
     vt = in % p.nv;
     if (w.cs) {
-      const int64_t per = (int64_t)C * w.L;
-      int a = 0, b = w.n;  // the last sequence whose first segment is <= seg
-      while (b - a > 1) {
-        const int m = (a + b) >> 1;
-        if (w.cs[m] / per + m <= seg) a = m; else b = m;
-      }
-      sq = a;
-      sg = (int)(seg - (w.cs[a] / per + a));
-      lo = w.cs[a];
-      hi = w.cs[a + 1];
+      sq = w.list[2 * seg];
+      if (sq < 0) return false;
+      sg = w.list[2 * seg + 1];
+      lo = w.cs[sq];
+      hi = w.cs[sq + 1];
+      seg = lo / ((int64_t)C * w.L) + sq + sg;
     } else {
       const int64_t per = p.nseg / w.n;
       sq = (int)(seg / per);
@@ -328,6 +324,7 @@ __device__ __forceinline__ void start_state(const WalkParams& p, const Chain& ch
   if (w.s0) each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
   if (!w.split || ch.head) return;
   const int cnt = rev ? ch.nsg - 1 - ch.sg : ch.sg;
+#pragma unroll 2
   for (int j = 0; j < cnt; ++j) {
     const int64_t s = ch.seg - ch.sg + (rev ? ch.nsg - 1 - j : j);
     const float d = w.seg_dec[(size_t)s * w.H + ch.h];
