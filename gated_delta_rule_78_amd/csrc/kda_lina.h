@@ -53,7 +53,7 @@ inline int64_t lina_pieces(int64_t rows, int64_t n, int64_t per) { return rows /
 hipError_t launch_lina_walk(const LinaWalk& w);
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream);
 hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int heads, int group, int d, bool bf16,
-                               void* stream);
+                               const int* end, void* stream);
 hipError_t launch_lina_ddecay(const LinaWalk& w, const float* a, const float* b, const float* e, int na, int ne,
                               const float* anchor, float* dg, double* part, float* dg_fixed);
 

@@ -27,10 +27,12 @@
 // token and stores them at once; K and V are read along the token axis with the LDS
 // transpose loads.
 //
-// Precision (bf16 inputs): sums, decays and the state are fp32.  Rounded to bf16 (2^-9
-// relative, as the output itself is) are P = r o QK^T and the state where it is multiplied
-// by q.  What enters the fp32 state, e^{G_C - G_j} v_j, goes through the matrix cores as a
-// bf16 pair (value and residual, 2^-18), and so does the state where a, b are taken from it.
+// Precision (bf16 inputs): sums, decays and the state are fp32.  Rounded to bf16 (off by at most
+// 2^-8 relative, as the output itself is) are P = r o QK^T and the state where it is multiplied
+// by q.  What enters the fp32 state, e^{G_C - G_j} v_j, goes through the matrix cores as a bf16
+// pair (value and residual, 2^-16); in the walks that a and b are taken from, it and the state
+// where it meets the row go as three bf16 terms (2^-24): D is a small difference of long sums
+// of a and b, and with pairs its error was 1e-5 of the gradient's norm, now 6e-7.
 #include "kda_lina_tile.h"
 
 namespace kda {
@@ -436,12 +438,14 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
   for (int64_t x = part[0] + tid; x < slots; x += NTB) list[2 * x] = -1;
 }
 
-// dq, dk of heads that share them: [rows, H, d] fp32 -> [rows, heads, d], summed in order
+// dq, dk of heads that share them: [rows, H, d] fp32 -> [rows, heads, d], summed in order; rows
+// behind a packed batch's last offset (*end) are left as they are
 template <typename T>
 __global__ __launch_bounds__(256) void lina_headsum_kernel(const float* __restrict__ part, void* __restrict__ out,
-                                                           int64_t quads, int heads, int group, int qd) {
+                                                           int64_t quads, int heads, int group, int qd,
+                                                           const int* __restrict__ end) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= quads) return;
+  if (i >= quads || (end && i >= (int64_t)*end * heads * qd)) return;
   const int64_t row = i / qd;  // (token, shared head)
   const int c = (int)(i % qd);
   const float4* src = (const float4*)part + (row * group) * qd + c;
@@ -565,17 +569,17 @@ hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int*
 }
 
 hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int heads, int group, int d, bool bf16,
-                               void* stream) {
+                               const int* end, void* stream) {
   const int64_t quads = rows * heads * (d / 4);
   if (quads == 0) return hipSuccess;
   const int64_t blocks = (quads + 255) / 256;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (bf16)
     hipLaunchKernelGGL(lina_headsum_kernel<bf16_t>, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, part,
-                       out, quads, heads, group, d / 4);
+                       out, quads, heads, group, d / 4, end);
   else
     hipLaunchKernelGGL(lina_headsum_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, part,
-                       out, quads, heads, group, d / 4);
+                       out, quads, heads, group, d / 4, end);
   return hipGetLastError();
 }
 

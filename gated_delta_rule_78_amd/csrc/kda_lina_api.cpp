@@ -258,6 +258,7 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
       return KDA_ERR_HIP;
   }
   const bool shared = s.H > Hk;
+  const int* end = packed ? a.cs + n_seqs : nullptr;
   float* share = (float*)(ws + l.off_share);
   float* anchor = (float*)(ws + l.off_anchor);
   float *da = (float*)(ws + l.off_a), *db = (float*)(ws + l.off_b), *de = (float*)(ws + l.off_e);
@@ -278,7 +279,7 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
     w.dots = da;
     w.snap = (float*)(ws + l.off_snap);
     if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
-    if (shared && kda::launch_lina_headsum(share, p.dq, toks, Hk, s.H / Hk, s.dk, a.bf16, stream) != hipSuccess)
+    if (shared && kda::launch_lina_headsum(share, p.dq, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) != hipSuccess)
       return KDA_ERR_HIP;
     // dk
     w.q = v;
@@ -291,7 +292,7 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
     w.dots = db;
     w.anchor = anchor;
     if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
-    if (shared && kda::launch_lina_headsum(share, p.dk, toks, Hk, s.H / Hk, s.dk, a.bf16, stream) != hipSuccess)
+    if (shared && kda::launch_lina_headsum(share, p.dk, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) != hipSuccess)
       return KDA_ERR_HIP;
   }
   kda::LinaWalk w = a;  // dv and the start state's gradient

@@ -446,7 +446,7 @@ int kda_gdn2_decode_tokens(const kda_shape* shape, const void* q, const void* k,
  *                    and NULL accepted, when the chains are walked whole; with fewer chains
  *                    than compute units it holds the end states of their segments)
  * Arithmetic: fp32 sums, decays and states; with bf16 inputs the products r o q.k and the state
- * as q meets it are rounded to bf16 (as o is), what is added to the state is not (2^-17).
+ * as q meets it are rounded to bf16 (as o is); what is added to the state is kept to 2^-16.
  * A non-finite v_t reaches the outputs from token t on only.  Alignment: 16 bytes for q, k, v,
  * o and the states, 4 for log_decay.  Aliasing, packed batches (cu_seqlens, n_seqs, states of
  * [n_seqs, H, dk, dv], token rows after the last offset not written) and errors as

@@ -1,0 +1,251 @@
+"""Linear attention and the query / key preparation: what the entry points refuse, on the host
+(CPU only: no call here reaches a kernel launch), and the fp64 references against differences."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import gated_delta_rule_78_amd as kda
+import lina_ref as ref
+
+OK, NULL, SHAPE, DTYPE, ALIGN, ALIAS, UNSUP, WORKSPACE = 0, -1, -2, -3, -4, -5, -6, -8
+BASE = 1 << 40
+MB = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(kda.LIB_PATH):
+        pytest.skip("libkda.so not built")
+    return kda.lib()
+
+
+def _p(i, off=0):  # never dereferenced: every call below is refused before a launch
+    return ctypes.c_void_p(BASE + i * 64 * MB + off)
+
+
+def _fwd(L, B=1, T=64, H=2, Hk=2, dk=64, dv=64, chunk=64, dtype=0, s0=None, sT=None, ws=None, nws=None, varlen=None,
+         cu=None, **kw):
+    sh = kda.Shape(B, T, H, dk, dv, chunk, dtype)
+    a = dict(q=_p(0), k=_p(1), v=_p(2), g=_p(3), o=_p(4))
+    a.update(kw)
+    ws = _p(9) if ws is None else ws
+    nws = 1 << 40 if nws is None else nws
+    tail = (a["q"], a["k"], a["v"], a["g"], 0, s0, a["o"], sT, ws, ctypes.c_size_t(nws), None)
+    if varlen is not None:
+        return L.kda_lina_chunk_fwd_varlen(ctypes.byref(sh), Hk, cu, varlen, *tail)
+    return L.kda_lina_chunk_fwd(ctypes.byref(sh), Hk, *tail)
+
+
+def _bwd(L, B=1, T=64, H=2, Hk=2, dk=64, dv=64, chunk=64, dtype=0, ws=None, nws=None, varlen=None, cu=None, **kw):
+    sh = kda.Shape(B, T, H, dk, dv, chunk, dtype)
+    a = dict(q=_p(0), k=_p(1), v=_p(2), g=_p(3), s0=_p(4), d_o=_p(5), dsT=_p(6), dq=_p(7), dk_=_p(8), dv_=_p(9),
+             dg=_p(10), ds0=_p(11))
+    a.update(kw)
+    ws = _p(12) if ws is None else ws
+    nws = 1 << 40 if nws is None else nws
+    tail = (a["q"], a["k"], a["v"], a["g"], 0, a["s0"], a["d_o"], a["dsT"], a["dq"], a["dk_"], a["dv_"], a["dg"],
+            a["ds0"], ws, ctypes.c_size_t(nws), None)
+    if varlen is not None:
+        return L.kda_lina_chunk_bwd_varlen(ctypes.byref(sh), Hk, cu, varlen, *tail)
+    return L.kda_lina_chunk_bwd(ctypes.byref(sh), Hk, *tail)
+
+
+def _dec(L, tokens=False, B=1, T=1, H=2, Hk=2, dk=64, dv=64, dtype=0, **kw):
+    sh = kda.Shape(B, T, H, dk, dv, 0, dtype)
+    a = dict(q=_p(0), k=_p(1), v=_p(2), g=_p(3), S=_p(4), o=_p(5))
+    a.update(kw)
+    f = L.kda_lina_decode_tokens if tokens else L.kda_lina_decode_step
+    return f(ctypes.byref(sh), Hk, a["q"], a["k"], a["v"], a["g"], 0, a["S"], a["o"], None)
+
+
+NUL = ctypes.c_void_p(None)
+
+
+@pytest.mark.parametrize("f", [_fwd, _bwd, _dec])
+def test_lina_refuses_shapes(L, f):
+    assert f(L, dtype=7) == DTYPE
+    assert f(L, H=0, Hk=1) == SHAPE and f(L, B=-1) == SHAPE and f(L, Hk=0) == SHAPE
+    assert f(L, H=4, Hk=3) == SHAPE and f(L, H=2, Hk=4) == SHAPE
+    assert f(L, H=65536, Hk=65536) == SHAPE
+    assert f(L, dk=96) == UNSUP and f(L, dv=32) == UNSUP
+    for name in ("q", "k", "v", "g"):
+        assert f(L, **{name: NUL}) == NULL, name
+
+
+def test_lina_refuses_sizes(L):
+    assert _fwd(L, T=-1) == SHAPE and _bwd(L, T=-1) == SHAPE and _dec(L, tokens=True, T=-1) == SHAPE
+    assert _fwd(L, B=1 << 16, T=1 << 16, H=2) == SHAPE
+    assert _fwd(L, chunk=32) == UNSUP and _bwd(L, chunk=32) == UNSUP
+
+
+def test_lina_refuses_alignment(L):
+    for name in ("q", "k", "v", "o"):
+        assert _fwd(L, **{name: _p(5, 8)}) == ALIGN
+    assert _fwd(L, g=_p(5, 2)) == ALIGN
+    assert _fwd(L, s0=_p(5, 4)) == ALIGN and _fwd(L, sT=_p(5, 4)) == ALIGN
+    for name in ("q", "k", "v", "d_o", "dq", "dk_", "dv_", "s0", "dsT", "ds0"):
+        assert _bwd(L, **{name: _p(13, 8)}) == ALIGN, name
+    assert _bwd(L, dg=_p(13, 2)) == ALIGN
+    assert _bwd(L, ws=_p(14, 16)) == ALIGN
+    assert _dec(L, S=_p(6, 8)) == ALIGN and _dec(L, q=_p(6, 1)) == ALIGN and _dec(L, g=_p(6, 2)) == ALIGN
+
+
+def test_lina_refuses_overlap(L):
+    for x in range(4):
+        assert _fwd(L, o=_p(x)) == ALIAS
+        assert _fwd(L, sT=_p(x)) == ALIAS
+        assert _dec(L, o=_p(x)) == ALIAS and _dec(L, S=_p(x)) == ALIAS
+    assert _fwd(L, s0=_p(5), sT=_p(5, 256)) == ALIAS
+    assert _dec(L, o=_p(4)) == ALIAS
+    for out in ("dq", "dk_", "dv_", "dg", "ds0"):
+        for x in range(7):
+            assert _bwd(L, **{out: _p(x)}) == ALIAS, (out, x)
+    assert _bwd(L, dq=_p(8)) == ALIAS and _bwd(L, dg=_p(11)) == ALIAS
+    assert _bwd(L, ws=_p(7)) == ALIAS
+
+
+def test_lina_workspaces(L):
+    sh = lambda **k: kda.Shape(*[dict(dict(B=1, T=64, H=2, dk=64, dv=64, chunk=64, dtype=0), **k)[n]
+                                 for n in ("B", "T", "H", "dk", "dv", "chunk", "dtype")])
+    size = lambda **k: L.kda_lina_chunk_fwd_workspace_size(ctypes.byref(sh(**k)))
+    assert size(T=64) == 0                      # one chunk: walked whole
+    assert size(B=8, T=8192, H=32) == 0         # 256 chains: walked whole
+    n = size(T=8192)
+    assert n > 0
+    assert _fwd(L, T=8192, nws=n - 1) == WORKSPACE and _fwd(L, T=8192, ws=NUL) == NULL
+    assert size(dk=96) == 0 and size(T=-1) == 0
+    b = L.kda_lina_chunk_bwd_workspace_size(ctypes.byref(sh()), 2)
+    assert b > 0 and _bwd(L, nws=b - 1) == WORKSPACE and _bwd(L, ws=NUL) == NULL
+    assert L.kda_lina_chunk_bwd_workspace_size(ctypes.byref(sh()), 1) > b  # shared heads are summed in it
+    assert L.kda_lina_chunk_bwd_workspace_size(ctypes.byref(sh()), 3) == 0
+    v = L.kda_lina_chunk_fwd_varlen_workspace_size(ctypes.byref(sh()), 3)
+    assert v > 0 and L.kda_lina_chunk_fwd_varlen_workspace_size(ctypes.byref(sh()), -1) == 0
+    assert _fwd(L, varlen=3, cu=_p(6), nws=v - 1) == WORKSPACE
+
+
+def test_lina_packed_refusals(L):
+    for f in (_fwd, _bwd):
+        assert f(L, varlen=3, cu=None) == NULL
+        assert f(L, varlen=-1, cu=_p(13)) == SHAPE
+        assert f(L, B=2, varlen=3, cu=_p(13)) == SHAPE
+        assert f(L, varlen=3, cu=_p(13, 2)) == ALIGN
+    assert _fwd(L, varlen=3, cu=_p(4)) == ALIAS and _bwd(L, varlen=3, cu=_p(7)) == ALIAS
+
+
+def _qk(L, bwd=False, tokens=64, Hq=2, Hk=1, d=64, qs=0, ks=0, norm=1, eps=1e-6, rot=64, inter=0, axes=1,
+        sec=(32, 0, 0, 0), p64=0, dtype=0, nws=1 << 30, **kw):
+    sh = kda.QkShape(tokens, Hq, Hk, d, qs, ks, norm, eps, 0.0, rot, inter, axes, (ctypes.c_int * 4)(*sec), p64, dtype)
+    a = dict(q=_p(0), k=_p(1), wq=_p(2), wk=_p(3), inv=_p(4), pos=_p(5), oq=_p(6), ok=_p(7), dyq=_p(8), dyk=_p(9),
+             dwq=_p(10), dwk=_p(11), ws=_p(12))
+    a.update(kw)
+    if bwd:
+        return L.kda_qk_norm_rope_bwd(ctypes.byref(sh), a["dyq"], a["dyk"], a["q"], a["k"], a["wq"], a["wk"], a["inv"],
+                                      a["pos"], a["oq"], a["ok"], a["dwq"], a["dwk"], a["ws"], ctypes.c_size_t(nws),
+                                      None)
+    return L.kda_qk_norm_rope(ctypes.byref(sh), a["q"], a["k"], a["wq"], a["wk"], a["inv"], a["pos"], a["oq"], a["ok"],
+                              None)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_qk_refusals(L, bwd):
+    f = lambda **k: _qk(L, bwd, **k)
+    assert f(dtype=5) == DTYPE
+    assert f(tokens=-1) == SHAPE and f(Hq=0) == SHAPE and f(Hk=-1) == SHAPE and f(Hq=70000) == SHAPE
+    assert f(eps=-1.0) == SHAPE and f(eps=float("nan")) == SHAPE
+    assert f(d=96) == UNSUP and f(norm=3) == UNSUP and f(norm=-1) == UNSUP
+    assert f(rot=128) == SHAPE and f(rot=-16) == SHAPE and f(rot=24, sec=(12, 0, 0, 0)) == UNSUP
+    assert f(axes=0) == UNSUP and f(axes=5) == UNSUP
+    assert f(axes=3, sec=(8, 12, 8, 0)) == SHAPE and f(axes=2, sec=(-8, 40, 0, 0)) == SHAPE
+    assert f(qs=127) == SHAPE and f(ks=63) == SHAPE and f(qs=132) == ALIGN
+    for nm in ("q", "k", "inv", "pos", "oq", "ok") + (("dyq", "dyk") if bwd else ()):
+        assert f(**{nm: NUL}) == NULL, nm
+    for nm in ("q", "k", "oq", "ok"):
+        assert f(**{nm: _p(13, 8)}) == ALIGN, nm
+    assert f(inv=_p(13, 4)) == ALIGN and f(pos=_p(13, 4), p64=1) == ALIGN and f(wq=_p(13, 2)) == ALIGN
+    for x in (1, 2, 3, 4, 5):
+        assert f(oq=_p(x)) == ALIAS, x
+    assert f(oq=_p(7)) == ALIAS
+    assert f(oq=_p(0, 256)) == ALIAS and f(oq=_p(0), qs=256) == ALIAS  # in place only onto the same dense rows
+    if bwd:
+        assert f(wq=NUL) == NULL and f(nws=16) == WORKSPACE and f(ws=NUL) == NULL and f(ws=_p(12, 16)) == ALIGN
+        assert f(dwq=_p(11)) == ALIAS and f(ws=_p(8)) == ALIAS
+
+
+def test_binding_refuses():
+    torch = pytest.importorskip("torch")
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt)
+    q, k, v, g = z(1, 8, 2, 64), z(1, 8, 2, 64), z(1, 8, 4, 64), z(1, 8, 4)
+    with pytest.raises(TypeError):
+        kda.lina_chunk_fwd(q, k.bfloat16(), v, g)
+    with pytest.raises(TypeError):
+        kda.lina_chunk_fwd(q, k, v, g.bfloat16())
+    with pytest.raises(TypeError):
+        kda.lina_chunk_fwd(q.half(), k.half(), v.half(), g)
+    for bad in (z(1, 8, 3), z(4, 1), z(5)):
+        with pytest.raises(ValueError):
+            kda.lina_chunk_fwd(q, k, v, bad)
+    with pytest.raises(ValueError):
+        kda.lina_chunk_fwd(q, k, z(1, 8, 3, 64), z(1, 8, 3))
+    with pytest.raises(ValueError):
+        kda.lina_chunk_fwd(q, k, v, g, initial_state=z(1, 2, 64, 64))
+    with pytest.raises(ValueError):
+        kda.lina_chunk_fwd(z(2, 8, 2, 64), z(2, 8, 2, 64), z(2, 8, 4, 64), z(2, 8, 4),
+                           cu_seqlens=torch.tensor([0, 8], dtype=torch.int32))
+    with pytest.raises(TypeError):
+        kda.lina_chunk_fwd(q, k, v, g, cu_seqlens=torch.tensor([0, 8]))
+    with pytest.raises(ValueError):
+        kda.lina_chunk_bwd(q, k, v, g, z(1, 8, 2, 64))
+    with pytest.raises(ValueError):
+        kda.lina_decode_step(q[:, 0], k[:, 0], v[:, 0], g[:, 0], z(1, 2, 64, 64))
+    with pytest.raises(ValueError):  # no CPU fallback
+        kda.lina_decode_step(q[:, 0], k[:, 0], v[:, 0], g[:, 0], z(1, 4, 64, 64))
+    with pytest.raises(ValueError):
+        kda.qk_norm_rope(q, k)
+    with pytest.raises(ValueError):
+        kda.qk_norm_rope(q, k, norm="layer")
+    with pytest.raises(ValueError):
+        kda.rope_inv_freq(63, device="cpu")
+    inv = kda.rope_inv_freq(64, device="cpu")
+    assert inv.dtype == torch.float64 and inv[0] == 1.0 and abs(float(inv[-1]) - 10000.0 ** (-62 / 64)) < 1e-16
+
+
+@pytest.mark.parametrize("seed", [0, 1])
+def test_lina_reference_gradient_against_differences(seed):
+    """The reference's gradients against central differences of its own loss, in fp64: with a
+    step of 1e-5 on values of order one, truncation (1e-10) and cancellation (1e-16 / 1e-5) stay
+    under 1e-8 of the loss's scale."""
+    r = np.random.default_rng(seed)
+    B, T, Hk, H, dk, dv = 2, 9, 2, 4, 5, 3
+    x = [r.standard_normal(s) for s in ((B, T, Hk, dk), (B, T, Hk, dk), (B, T, H, dv), (B, T, H), (B, H, dk, dv))]
+    x[3] = -0.5 * np.abs(x[3])
+    u, w = r.standard_normal((B, T, H, dv)), r.standard_normal((B, H, dk, dv))
+
+    def loss(q, k, v, g, s):
+        o, sT = ref.lina_fwd(q, k, v, g, s)
+        return (o * u).sum() + (sT * w).sum()
+
+    q, k, v, g, s = x
+    grads = ref.lina_bwd(q, k, v, g, u, s, w)
+    for i, gr in enumerate(grads):
+        d = r.standard_normal(x[i].shape)
+        h = 1e-5
+        hi, lo = [list(x) for _ in range(2)]
+        hi[i], lo[i] = x[i] + h * d, x[i] - h * d
+        num = (loss(*hi) - loss(*lo)) / (2 * h)
+        assert abs(num - (gr * d).sum()) <= 1e-7 * (1 + np.abs(gr * d).sum()), i
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2", None])
+@pytest.mark.parametrize("inter", [False, True])
+def test_qk_reference_gradient_against_differences(norm, inter):
+    r = np.random.default_rng(3)
+    x, w, dy = r.standard_normal((6, 2, 32)), r.standard_normal(32), r.standard_normal((6, 2, 32))
+    pos, inv, sec = r.integers(0, 50, (3, 6)), 10.0 ** -np.linspace(0, 3, 8), (2, 3, 3)
+    f = lambda x, w: (ref.qk_fwd(x, w, pos, inv, sec, inter, norm, 1e-3) * dy).sum()
+    dx, dw = ref.qk_bwd(dy, x, w, pos, inv, sec, inter, norm, 1e-3)
+    h = 1e-5
+    d, e = r.standard_normal(x.shape), r.standard_normal(w.shape)
+    assert abs((f(x + h * d, w) - f(x - h * d, w)) / (2 * h) - (dx * d).sum()) <= 1e-7 * np.abs(dx * d).sum()
+    assert abs((f(x, w + h * e) - f(x, w - h * e)) / (2 * h) - (dw * e).sum()) <= 1e-7 * np.abs(dw * e).sum()
