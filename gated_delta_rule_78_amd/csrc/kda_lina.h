@@ -51,6 +51,8 @@ constexpr int kLinaGroup = 16;  // chunks between two kept states of the backwar
 inline int64_t lina_pieces(int64_t rows, int64_t n, int64_t per) { return rows / (64 * per) + n; }
 
 hipError_t launch_lina_walk(const LinaWalk& w);
+// dk's and dv's walk in one kernel: bf16, widths equal; wv.x: v
+hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv);
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream);
 hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int heads, int group, int d, bool bf16,
                                const int* end, void* stream);

@@ -33,6 +33,8 @@
 // pair (value and residual, 2^-16); in the walks that a and b are taken from, it and the state
 // where it meets the row go as three bf16 terms (2^-24): D is a small difference of long sums
 // of a and b, and with pairs its error was 1e-5 of the gradient's norm, now 6e-7.
+#include <type_traits>
+
 #include "kda_lina_tile.h"
 
 namespace kda {
@@ -166,9 +168,9 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       if constexpr (DOT == kDotCross)
         if (wave == 0) store_dots<DOT, REV>(p, ch, c, sdot[it & 1], sdot2[it & 1], lane);
       Frag<T> fv[2];
-      tok_frag<T, VT>(fv[0], tV(it), 16 * wave, 0, lane);
-      tok_frag<T, VT>(fv[1], tV(it), 16 * wave, 1, lane);
-      add_intra<T, DK>(acc, fv, tP(it), tV(it), wave, lane);
+      tok_frag<T, VT>(fv[0], tV(it), tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
+      tok_frag<T, VT>(fv[1], tV(it), tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
+      add_intra<T, VT>(acc, fv, tP(it), tV(it), 16 * wave, lane);
       store_out<T, REV>(acc, w, ch, c, wave, lane);
       add_chunk<T, DK, DOT == kDotRow>(S, fv, tK(it), dc, lane);
       if constexpr (DOT == kDotRow && REV)
@@ -176,6 +178,212 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       lds_barrier();
     }
     store_state<DK, REV>(p, ch, tid, S);
+  }
+}
+
+// The two reverse walks of the backward in one, for d_k = d_v = D (bf16): dk = walk(Q = v, K = u,
+// V = q) and dv = walk(Q = k, K = q, V = u) meet the same four tiles, so these are fetched and
+// written to LDS once, and the pair sums M = r o (q k^T) o (u v^T) come from the two score
+// matrices the walks need anyway.  Twelve waves, three to a SIMD: four keep 64 columns of the
+// transposed state and make dk, four 64 columns of the state and make dv, four fetch, write and
+// make the scores of the next chunk.  A step has two halves: from the states (meanwhile the next
+// tiles and this chunk's P go to LDS), then P V and the states' update (meanwhile the next scores,
+// kept in registers).  With separate walks B4 H32 T8K took 0.87 ms here.
+template <int D, bool WANT>
+struct RevLds {
+  static constexpr int Q = 0, K = Tile<bf16_t, D>::BYTES, V = 2 * K, U = 3 * K, TILES = 4 * K;
+  static constexpr int PK = 2 * TILES, PV = PK + Tile<bf16_t, 64>::BYTES;
+  static constexpr int BYTES = PV + Tile<bf16_t, 64>::BYTES;
+};
+
+struct RevParams {
+  WalkParams k, v;  // the walks of dk and dv
+};
+
+template <int D, bool WANT>
+__global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p) {
+  typedef bf16_t T;
+  typedef RevLds<D, WANT> Lds;
+  constexpr int KS = D / 32;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ Decays dec[2];
+  __shared__ __align__(16) float srow[WANT ? 4 : 1][C], scol[WANT ? 4 : 1][C];
+  __shared__ float sown[WANT ? C : 1];
+  auto tile = [&](int it, int at) { return smem + (it & 1) * Lds::TILES + at; };
+
+  const int tid = threadIdx.x & (NT - 1), lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
+  Chain ch;
+  if (!ch.place(p.k, true)) return;
+  const int steps = ch.last - ch.first;
+  auto chunk = [&](int it) { return ch.last - 1 - it; };
+  const int role = threadIdx.x / NT;
+
+  if (role == 2) {
+    if (steps == 0) return;
+    const LinaWalk& w = p.v.w;
+    const Operand<T> v(w.x, w, ch.h, D, 0), u(w.v, w, ch.h, D, 0);
+    Stage<T, D, true> rv, ru;
+    float lg = 0.f;
+    const bool sums = WANT && ch.vt == 0;  // the scores are whole: one workgroup's sums of M do
+    auto fetch = [&](int it) {
+      const int c = chunk(it);
+      const int64_t t = ch.lo + (int64_t)c * C;
+      const uint32_t have = ch.rows(c);
+      if (wave == 1) lg = row_decay<true>(w, ch, c, lane);
+      ru.load(u.rows(t, have), u.step, true, tid);
+      rv.load(v.rows(t, have), v.step, true, tid);
+    };
+    auto put = [&](int it) {
+      if (wave == 1) chunk_decays(dec[it & 1], lg, lane);
+      ru.store(tile(it, Lds::U), tid);
+      rv.store(tile(it, Lds::V), tid);
+    };
+    uint2 pk[4], pv[4];  // the wave's rows of both P, on their way to LDS
+    auto scores = [&](int it) {
+      const Decays& dc = dec[it & 1];
+      const int row = 16 * wave + n;
+      Frag<T> fv[KS], fk[KS];
+      const uint32_t rb = row_base<T, D, true>(lane);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        row_frag<T, D>(fv[s], tile(it, Lds::V), rb, 16 * wave, s);
+        row_frag<T, D>(fk[s], tile(it, Lds::K), rb, 16 * wave, s);
+      }
+      const float ih = dc.hi[row], il = dc.lo[row];
+      float own = 0.f;
+#pragma unroll
+      for (int J = 0; J < 4; ++J) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+        if (J <= wave) {
+          f32x4_t a = zero4(), b = zero4();
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            Frag<T> f;
+            row_frag<T, D>(f, tile(it, Lds::U), rb, 16 * J, s);
+            mma(a, f, fv[s]);
+            row_frag<T, D>(f, tile(it, Lds::Q), rb, 16 * J, s);
+            mma(b, f, fk[s]);
+          }
+          const float4 jh = *(const float4*)&dc.hi[16 * J + 4 * g], jl = *(const float4*)&dc.lo[16 * J + 4 * g];
+          const float jhs[4] = {jh.x, jh.y, jh.z, jh.w}, jls[4] = {jl.x, jl.y, jl.z, jl.w};
+          float m[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = 16 * J + 4 * g + i;
+            const float r = fast_exp2((ih - jhs[i]) + (il - jls[i]));
+            x[i] = j <= row ? a[i] * r : 0.f;
+            y[i] = j <= row ? b[i] * r : 0.f;
+            m[i] = j < row ? (a[i] * r) * b[i] : 0.f;
+          }
+          if (sums) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              own += m[i];
+              m[i] = row16_sum(m[i]);
+            }
+            if (n == 0) *(float4*)&scol[wave][16 * J + 4 * g] = make_float4(m[0], m[1], m[2], m[3]);
+          }
+        }
+        pk[J] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        pv[J] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      }
+      if (sums) {
+        own += __shfl_xor(own, 16);
+        own += __shfl_xor(own, 32);
+        if (g == 0) sown[row] = own;
+      }
+    };
+    fetch(0);
+    put(0);
+    if (steps > 1) fetch(1);
+    lds_barrier();
+    scores(0);
+    lds_barrier();
+    for (int it = 0; it < steps; ++it) {
+      const uint32_t pb = row_base<T, 64, true>(lane);
+#pragma unroll
+      for (int J = 0; J < 4; ++J)
+        if (J <= (wave | 1)) {
+          const uint32_t at = 16 * wave * Tile<T, 64>::RB + (pb ^ (J * 32));
+          *(uint2*)(smem + Lds::PK + at) = pk[J];
+          *(uint2*)(smem + Lds::PV + at) = pv[J];
+        }
+      if constexpr (WANT)
+        if (sums && wave == 0) store_dots<kDotCross, true>(p.v, ch, chunk(it), scol, sown, lane);
+      if (it + 1 < steps) put(it + 1);
+      if (it + 2 < steps) fetch(it + 2);
+      lds_barrier();
+      if constexpr (WANT)
+        if (wave == 0) store_dots<kDotRow, true>(p.k, ch, chunk(it), srow, sown, lane);
+      if (it + 1 < steps) scores(it + 1);
+      lds_barrier();
+    }
+    return;
+  }
+
+  // dk: rows of v and u against q; dv: rows of k and q against u
+  auto walk = [&](const WalkParams& wp, int tq, int tk, int tv, int tx, int tp, auto exact, auto fetch, auto put) {
+    constexpr bool EXACT = decltype(exact)::value;
+    const int c0 = ch.vt * VT + 16 * wave;
+    f32x4_t S[D / 16];
+    if (steps > 0) fetch(0);
+    start_state<D>(wp, ch, true, tid, S);
+    if (steps > 0) {
+      put(0);
+      if (steps > 1) fetch(1);
+      lds_barrier();
+      lds_barrier();
+    }
+    for (int it = 0; it < steps; ++it) {
+      const int c = chunk(it);
+      const Decays& dc = dec[it & 1];
+      if (it + 1 < steps) put(it + 1);
+      if (it + 2 < steps) fetch(it + 2);
+      f32x4_t acc[4];
+      from_state<T, D, EXACT, true>(S, tile(it, tq), lane, acc);
+      scale_rows(acc, dc, lane);
+      if constexpr (EXACT) {  // with the rows of k: b
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float x[4];
+          ld_quad<T>(tile(it, tx) + Tile<T, D>::quad(16 * t + n, c0 / 4 + g), 0, x);
+          float d = acc[t][0] * x[0] + acc[t][1] * x[1] + acc[t][2] * x[2] + acc[t][3] * x[3];
+          d += __shfl_xor(d, 16);
+          d += __shfl_xor(d, 32);
+          if (g == 0) srow[wave][16 * t + n] = d;
+        }
+      }
+      Frag<T> fv[2];
+      tok_frag<T, D>(fv[0], tile(it, tv), tok_base<T, D, true>(lane), c0, 0, lane);
+      tok_frag<T, D>(fv[1], tile(it, tv), tok_base<T, D, true>(lane), c0, 1, lane);
+      lds_barrier();
+      add_intra<T, D, true>(acc, fv, smem + tp, tile(it, tv), c0, lane);
+      store_out<T, true, true>(acc, wp.w, ch, c, wave, lane);
+      add_chunk<T, D, EXACT, true>(S, fv, tile(it, tk), dc, lane);
+      if constexpr (EXACT)
+        if (c % kLinaGroup == 0) store_anchor<D>(wp, ch, c, tid, S);
+      lds_barrier();
+    }
+    store_state<D, true>(wp, ch, tid, S);
+  };
+  if (role == 0) {
+    walk(p.k, Lds::V, Lds::U, Lds::Q, Lds::K, Lds::PK, std::integral_constant<bool, WANT>{}, [](int) {}, [](int) {});
+  } else {  // with the fewer products, these waves fetch q and k as well
+    const LinaWalk& w = p.v.w;
+    const Operand<T> q(w.k, w, ch.h, D, 0), k(w.q, w, ch.h, D, 0);
+    Stage<T, D, true> rq, rk;
+    walk(
+        p.v, Lds::K, Lds::Q, Lds::U, Lds::V, Lds::PV, std::false_type{},
+        [&](int it) {
+          const int c = chunk(it);
+          const int64_t t = ch.lo + (int64_t)c * C;
+          rq.load(q.rows(t, ch.rows(c)), q.step, true, tid);
+          rk.load(k.rows(t, ch.rows(c)), k.step, true, tid);
+        },
+        [&](int it) {
+          rq.store(tile(it, Lds::Q), tid);
+          rk.store(tile(it, Lds::K), tid);
+        });
   }
 }
 
@@ -252,9 +460,9 @@ __global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
     if constexpr (DOT != kDotNone)
       if (wave == 1) store_dots<DOT, REV>(p, ch, c, sdot, sdot2, lane);
     Frag<T> fv[2];
-    tok_frag<T, VT>(fv[0], sV, 16 * wave, 0, lane);
-    tok_frag<T, VT>(fv[1], sV, 16 * wave, 1, lane);
-    add_intra<T, DK>(acc, fv, sP, sV, wave, lane);
+    tok_frag<T, VT>(fv[0], sV, tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
+    tok_frag<T, VT>(fv[1], sV, tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
+    add_intra<T, VT>(acc, fv, sP, sV, 16 * wave, lane);
     store_out<T, REV>(acc, w, ch, c, wave, lane);
     add_chunk<T, DK, false>(S, fv, sK, dc, lane);
     if constexpr (DOT == kDotRow && REV)
@@ -310,8 +518,8 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
     const Decays& dc = dec[it & 1];
     const char* t = smem + (it & 1) * TILES;
     Frag<T> fv[2];
-    tok_frag<T, VT>(fv[0], t + Tile<T, DK>::BYTES, 16 * wave, 0, lane);
-    tok_frag<T, VT>(fv[1], t + Tile<T, DK>::BYTES, 16 * wave, 1, lane);
+    tok_frag<T, VT>(fv[0], t + Tile<T, DK>::BYTES, tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
+    tok_frag<T, VT>(fv[1], t + Tile<T, DK>::BYTES, tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
     total *= dc.tot;
     add_chunk<T, DK, EXACT>(S, fv, t, dc, lane);
     lds_barrier();
@@ -322,15 +530,19 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
   if (tid == 0 && ch.vt == 0) w.seg_dec[(size_t)ch.seg * w.H + ch.h] = total;
 }
 
-template <typename K>
-hipError_t launch(K kern, const WalkParams& p, int threads, int lds) {
-  const unsigned blocks = walk_blocks(p);
+inline const WalkParams& chain_of(const WalkParams& p) { return p; }
+inline const WalkParams& chain_of(const RevParams& p) { return p.k; }
+
+template <typename K, typename P>
+hipError_t launch(K kern, const P& p, int threads, int lds) {
+  const WalkParams& c = chain_of(p);
+  const unsigned blocks = walk_blocks(c);
   if (blocks == 0) return hipErrorInvalidValue;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kern, dim3(blocks), dim3(threads), lds, (hipStream_t)p.w.stream, p);
+  hipLaunchKernelGGL(kern, dim3(blocks), dim3(threads), lds, (hipStream_t)c.w.stream, p);
   return hipGetLastError();
 }
 
@@ -560,6 +772,31 @@ hipError_t launch_lina_walk(const LinaWalk& w) {
   }
   if (w.bf16) return w.dk == 128 ? walk_bf16<128>(p) : walk_bf16<64>(p);
   return w.dk == 128 ? walk_f32<128>(p) : walk_f32<64>(p);
+}
+
+hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv) {
+  RevParams p;
+  p.k.w = wk;
+  p.v.w = wv;
+  for (WalkParams* x : {&p.k, &p.v}) {
+    LinaWalk& w = x->w;
+    w.rev = true;
+    x->nv = w.dv / VT;
+    x->rows = w.cs ? w.T : (int64_t)w.n * w.T;
+    const int64_t nch = ((int64_t)w.T + C - 1) / C;
+    x->nseg = w.cs ? lina_pieces(w.T, w.n, w.L) : (int64_t)w.n * (nch > 0 ? (nch + w.L - 1) / w.L : 1);
+    if (x->nseg == 0) return hipSuccess;
+    if (w.split) {
+      const hipError_t e = w.dk == 128 ? segments<bf16_t, 128>(*x) : segments<bf16_t, 64>(*x);
+      if (e != hipSuccess) return e;
+    }
+  }
+  const bool want = wk.dot != kDotNone;
+  if (wk.dk == 128)
+    return want ? launch(lina_reverse_kernel<128, true>, p, 3 * NT, RevLds<128, true>::BYTES)
+                : launch(lina_reverse_kernel<128, false>, p, 3 * NT, RevLds<128, false>::BYTES);
+  return want ? launch(lina_reverse_kernel<64, true>, p, 3 * NT, RevLds<64, true>::BYTES)
+              : launch(lina_reverse_kernel<64, false>, p, 3 * NT, RevLds<64, false>::BYTES);
 }
 
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream) {

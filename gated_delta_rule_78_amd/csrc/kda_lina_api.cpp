@@ -161,7 +161,7 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
 struct BwdLayout {
   Plan plan;
   int64_t groups;
-  size_t off_dec, off_cs, off_list, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
+  size_t off_dec, off_seg2, off_dec2, off_cs, off_list, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
 };
 
 BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
@@ -172,7 +172,9 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   const int64_t per = 64 * kda::kLinaGroup;
   l.groups = n_seqs >= 0 ? kda::lina_pieces(s.T, n, kda::kLinaGroup) : n * ((s.T + per - 1) / per);
   l.off_dec = up(seg * state);
-  l.off_cs = up(l.off_dec + seg * s.H * 4);
+  l.off_seg2 = up(l.off_dec + seg * s.H * 4);
+  l.off_dec2 = up(l.off_seg2 + seg * state);
+  l.off_cs = up(l.off_dec2 + seg * s.H * 4);
   l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
   l.off_snap = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
   l.off_anchor = up(l.off_snap + l.groups * state);
@@ -263,6 +265,7 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
   float* anchor = (float*)(ws + l.off_anchor);
   float *da = (float*)(ws + l.off_a), *db = (float*)(ws + l.off_b), *de = (float*)(ws + l.off_e);
   const kda::LinaOp q{p.q, Hk}, k{p.k, Hk}, v{p.v, s.H}, u{p.d_o, s.H};
+  kda::LinaWalk wk;
   if (toks > 0) {
     kda::LinaWalk w = a;  // dq
     w.q = u;
@@ -281,19 +284,16 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
     if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
     if (shared && kda::launch_lina_headsum(share, p.dq, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) != hipSuccess)
       return KDA_ERR_HIP;
-    // dk
-    w.q = v;
-    w.k = u;
-    w.v = q;
-    w.x = k;
-    w.out = shared ? (void*)share : p.dk;
-    w.s0 = p.dsT;
-    w.rev = true;
-    w.dots = db;
-    w.anchor = anchor;
-    if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
-    if (shared && kda::launch_lina_headsum(share, p.dk, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) != hipSuccess)
-      return KDA_ERR_HIP;
+    wk = w;  // dk
+    wk.q = v;
+    wk.k = u;
+    wk.v = q;
+    wk.x = k;
+    wk.out = shared ? (void*)share : p.dk;
+    wk.s0 = p.dsT;
+    wk.rev = true;
+    wk.dots = db;
+    wk.anchor = anchor;
   }
   kda::LinaWalk w = a;  // dv and the start state's gradient
   w.q = k;
@@ -308,9 +308,17 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
   w.rev = true;
   w.dot = p.dg ? kda::kDotCross : kda::kDotNone;
   w.dots = de;
-  if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
+  w.seg_state = (float*)(ws + l.off_seg2);
+  w.seg_dec = (float*)(ws + l.off_dec2);
+  const bool fused = a.bf16 && s.dk == s.dv;
+  if (toks > 0) {
+    if ((fused ? kda::launch_lina_reverse(wk, w) : kda::launch_lina_walk(wk)) != hipSuccess) return KDA_ERR_HIP;
+    if (shared && kda::launch_lina_headsum(share, p.dk, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) != hipSuccess)
+      return KDA_ERR_HIP;
+  }
+  if (!(toks > 0 && fused) && kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
   if (p.dg && toks > 0 &&
-      kda::launch_lina_ddecay(w, da, db, de, s.dk / 64, s.dv / 64, anchor, p.per_head ? nullptr : p.dg,
+      kda::launch_lina_ddecay(w, da, db, de, s.dk / 64, fused ? 1 : s.dv / 64, anchor, p.per_head ? nullptr : p.dg,
                               (double*)(ws + l.off_part), p.per_head ? p.dg : nullptr) != hipSuccess)
     return KDA_ERR_HIP;
   return KDA_OK;

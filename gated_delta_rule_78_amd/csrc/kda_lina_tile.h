@@ -15,14 +15,30 @@ constexpr int NT = 256;  // threads that hold a workgroup's state, and threads t
 typedef short v4s_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s_t lds_v4s;
 
+// LEAN: x, but not known to be the same each time, so that the addresses made from it stay out of
+// the registers that live through a loop.  The kernel with three waves to a SIMD (168 registers)
+// spilled without it; the one with two (256) is 3% faster with its addresses kept.
+template <bool LEAN>
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
+#ifndef KDA_HOST_PASS
+  if constexpr (LEAN) asm volatile("" : "+v"(x));
+#endif
+  return x;
+}
+
 // 64-row LDS tile of D elements a row, in quads of four elements.  Units of 16 bytes are
-// permuted by the row so that the three ways of reading it (16 rows at one quad, four plus
-// four rows at one 16-column block by the transpose loads, 16 rows at two quads) touch all
-// banks evenly.
+// permuted (exclusive or) by the row so that the three ways of reading it (16 rows at one quad,
+// four plus four rows at one 16-column block by the transpose loads, 16 rows at two quads) touch
+// all banks evenly: measured at the rate of a linear read.  The permutation depends on the row
+// within 16 only, so every address is a lane's base, an exclusive or and a constant.  (Rows
+// padded instead, with every address a base and a constant, cost more in conflicts than they
+// saved: B4 H32 T8K forward 303 us against 294.)
 template <typename T, int D>
 struct Tile {
+  static constexpr int DIM = D;
   static constexpr int RB = D * (int)sizeof(T);
   static constexpr int BYTES = C * RB;
+  static constexpr int QB = 4 * (int)sizeof(T);
   __device__ __forceinline__ static int unit(int row, int u) {
     if constexpr (sizeof(T) == 4) return row * RB + (((u & ~15) | ((u ^ row) & 15)) << 4);
     else if constexpr (D == 128) return row * RB + ((u ^ (((row & 3) << 1) | (row & 8) | ((row >> 2) & 1))) << 4);
@@ -37,37 +53,59 @@ struct Tile {
   }
 };
 
-// row fragment of 32 channels: slots 0-3 channels 32 s + 4 g.., slots 4-7 channels 32 s + 16 + 4 g..
-// of row `row`: the order in which two 16-row accumulator tiles of the state hold their rows
-template <typename T, int D>
-__device__ __forceinline__ void row_frag(Frag<T>& f, const char* t, int row, int s, int g) {
-  f.load4x2(t + Tile<T, D>::quad(row, 8 * s + g), t + Tile<T, D>::quad(row, 8 * s + 4 + g));
+// A lane's bases in a tile, by what it reads.
+template <typename T, int D, bool LEAN>
+__device__ __forceinline__ uint32_t row_base(int lane) {  // row n, quad g
+  return fresh<LEAN>(Tile<T, D>::quad(lane & 15, lane >> 4));
+}
+template <typename T, int D, bool LEAN>
+__device__ __forceinline__ uint32_t tok_base(int lane) {  // bf16: row 8 g + n / 4, quad n % 4
+  const int g = lane >> 4, n = lane & 15;
+  return sizeof(T) == 2 ? fresh<LEAN>(Tile<T, D>::quad(8 * g + (n >> 2), n & 3)) : 0;
 }
 
-// token fragment: slots hold tokens 32 s + 8 g + e of column c0 + n
+// row fragment of 32 columns: slots 0-3 columns 32 s + 4 g.., slots 4-7 columns 32 s + 16 + 4 g.. of
+// row r0 + n (r0 a multiple of 16): the order in which two 16-row accumulator tiles of the state
+// hold their rows
 template <typename T, int D>
-__device__ __forceinline__ void tok_frag(Frag<T>& f, const char* t, int c0, int s, int lane) {
-  const int g = lane >> 4, n = lane & 15;
+__device__ __forceinline__ void row_frag(Frag<T>& f, const char* t, uint32_t base, int r0, int s) {
+  const char* p = t + r0 * Tile<T, D>::RB;
+  f.load4x2(p + (base ^ (s * 32 * sizeof(T))), p + (base ^ ((s * 32 + 16) * sizeof(T))));
+}
+
+// token fragment: slots hold tokens 32 s + 8 g + e of column c0 + n (c0 a multiple of 16)
+template <typename T, int D>
+__device__ __forceinline__ void tok_frag(Frag<T>& f, const char* t, uint32_t base, int c0, int s, int lane) {
   if constexpr (sizeof(T) == 2) {
 #ifndef KDA_HOST_PASS
-    // 16 lanes read four rows of 16 columns and get four rows of their own column
-    const int q = c0 / 4 + (n & 3), r = 32 * s + 8 * g + (n >> 2);
-    const v4s_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(t + Tile<T, D>::quad(r, q)));
-    const v4s_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(t + Tile<T, D>::quad(r + 4, q)));
+    // 16 lanes read four rows of 16 columns and get four rows of their own column; four rows
+    // further the permutation differs in its lowest bit
+    const char* p = t + 32 * s * Tile<T, D>::RB;
+    const uint32_t o = base ^ (c0 * 2);
+    const v4s_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + o));
+    const v4s_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + (o ^ 16) + 4 * Tile<T, D>::RB));
     const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
     f.w[0] = x.x; f.w[1] = x.y; f.w[2] = y.x; f.w[3] = y.y;
 #endif
   } else {
-    const int c = c0 + n;
+    const int g = lane >> 4, c = c0 + (lane & 15);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f.w[e] = *(const float*)(t + Tile<T, D>::quad(32 * s + 8 * g + e, c >> 2) + (c & 3) * 4);
   }
 }
 
-// slots hold columns 32 s + 8 g + e of row `row`
+// slots hold columns 32 s + 8 g + e of row r0 + n (r0 a multiple of 16) of a 64-column tile;
+// base: row n, quad 2 g
+template <typename T, bool LEAN>
+__device__ __forceinline__ uint32_t col_base(int lane) {
+  return fresh<LEAN>(Tile<T, 64>::quad(lane & 15, 2 * (lane >> 4)));
+}
 template <typename T>
-__device__ __forceinline__ void col_frag(Frag<T>& f, const char* t, int row, int s, int g) {
-  f.load4x2(t + Tile<T, 64>::quad(row, 8 * s + 2 * g), t + Tile<T, 64>::quad(row, 8 * s + 2 * g + 1));
+__device__ __forceinline__ void col_frag(Frag<T>& f, const char* t, uint32_t base, int r0, int s) {
+  const char* p = t + r0 * Tile<T, 64>::RB;
+  const uint32_t o = base ^ (s * 32 * sizeof(T));
+  if constexpr (sizeof(T) == 2) f.load8(p + o);
+  else f.load4x2(p + o, p + (o ^ 16));
 }
 
 template <typename T>
@@ -348,25 +386,28 @@ __device__ __forceinline__ void store_state(const WalkParams& p, const Chain& ch
   each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { w.sT[at] = S[ct][i] * d; });
 }
 
+// byte offset of row r (rows counted from the end in a reverse walk), and of `rows` rows
+__device__ __forceinline__ uint32_t row_off(bool rev, int r, uint32_t step) { return (rev ? C - 1 - r : r) * step; }
+__device__ __forceinline__ uint32_t rows_off(bool rev, int rows, uint32_t step) { return (rev ? -rows : rows) * step; }
+
 // A thread's share of one chunk's tiles, on its way from memory to LDS (NT threads).
-template <typename T, int D>
+template <typename T, int D, bool LEAN = false>
 struct Stage {
-  static constexpr int N = C * D * (int)sizeof(T) / 16 / NT;
   static constexpr int RU = Tile<T, D>::RB / 16;  // 16-byte units of a row
+  static constexpr int N = C * RU / NT;
+  static constexpr int ROWS = NT / RU;            // rows at a time, a multiple of 16 for bf16
   u32x4_t r[N];
   __device__ __forceinline__ void load(const Rows& b, uint32_t step, bool rev, int tid) {
+    const uint32_t o = fresh<LEAN>(row_off(rev, tid / RU, step) + tid % RU * 16);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = tid + NT * i, row = u / RU;
-      r[i] = b.load16((rev ? C - 1 - row : row) * step + u % RU * 16);
-    }
+    for (int i = 0; i < N; ++i) r[i] = b.load16(o + rows_off(rev, ROWS * i, step));
   }
   __device__ __forceinline__ void store(char* t, int tid) const {
+    const uint32_t o = fresh<LEAN>(Tile<T, D>::unit(tid / RU, tid % RU));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = tid + NT * i;
-      *(u32x4_t*)(t + Tile<T, D>::unit(u / RU, u % RU)) = r[i];
-    }
+    for (int i = 0; i < N; ++i)
+      *(u32x4_t*)(t + (ROWS % 16 == 0 ? o + ROWS * i * Tile<T, D>::RB
+                                      : Tile<T, D>::unit(tid / RU + ROWS * i, tid % RU))) = r[i];
   }
 };
 
@@ -379,11 +420,12 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
   constexpr int KS = DK / 32;
   const int g = lane >> 4, n = lane & 15, row = 16 * wave + n;
   Frag<T> fq[KS], fx[DOT == kDotCross ? 2 : 1];
+  const uint32_t rb = row_base<T, DK, false>(lane), vb = row_base<T, VT, false>(lane);
 #pragma unroll
-  for (int s = 0; s < KS; ++s) row_frag<T, DK>(fq[s], sQ, row, s, g);
+  for (int s = 0; s < KS; ++s) row_frag<T, DK>(fq[s], sQ, rb, 16 * wave, s);
   if constexpr (DOT == kDotCross) {
-    row_frag<T, VT>(fx[0], sX, row, 0, g);
-    row_frag<T, VT>(fx[1], sX, row, 1, g);
+    row_frag<T, VT>(fx[0], sX, vb, 16 * wave, 0);
+    row_frag<T, VT>(fx[1], sX, vb, 16 * wave, 1);
   }
   const float ih = dc.hi[row], il = dc.lo[row];
   float own_sum = 0.f;
@@ -395,14 +437,14 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         Frag<T> fk;
-        row_frag<T, DK>(fk, sK, 16 * J + n, s, g);
+        row_frag<T, DK>(fk, sK, rb, 16 * J, s);
         mma(a, fk, fq[s]);
       }
       if constexpr (DOT == kDotCross) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           Frag<T> fv;
-          row_frag<T, VT>(fv, sV, 16 * J + n, s, g);
+          row_frag<T, VT>(fv, sV, vb, 16 * J, s);
           mma(e, fv, fx[s]);
         }
       }
@@ -421,7 +463,7 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
         }
       }
     }
-    if (J <= (wave | 1)) st_quad<T>(sP + Tile<T, 64>::quad(row, 4 * J + g), x);
+    if (J <= (wave | 1)) st_quad<T>(sP + 16 * wave * Tile<T, 64>::RB + (vb ^ (J * 16 * sizeof(T))), x);
   }
   if constexpr (DOT == kDotCross) {
     own_sum += __shfl_xor(own_sum, 16);
@@ -432,9 +474,9 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
 
 // The start state's part of the outputs, before the decay to the token: rows of S^T against rows
 // of Q.  acc[t] holds columns 4 g + i of token 16 t + n.  EXACT: the state in three bf16 terms.
-template <typename T, int DK, bool EXACT>
+template <typename T, int DK, bool EXACT, bool LEAN = false>
 __device__ __forceinline__ void from_state(const f32x4_t (&S)[DK / 16], const char* sQ, int lane, f32x4_t (&acc)[4]) {
-  const int g = lane >> 4, n = lane & 15;
+  const uint32_t rb = row_base<T, DK, LEAN>(lane);
 #pragma unroll
   for (int t = 0; t < 4; ++t) acc[t] = zero4();
 #pragma unroll
@@ -450,7 +492,7 @@ __device__ __forceinline__ void from_state(const f32x4_t (&S)[DK / 16], const ch
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       Frag<T> fq;
-      row_frag<T, DK>(fq, sQ, 16 * t + n, s, g);
+      row_frag<T, DK>(fq, sQ, rb, 16 * t, s);
       mma(acc[t], fs, fq);
       if constexpr (sizeof(T) == 2 && EXACT) {
         mma(acc[t], fm, fq);
@@ -460,11 +502,13 @@ __device__ __forceinline__ void from_state(const f32x4_t (&S)[DK / 16], const ch
   }
 }
 
-// acc (the start state's part) += P V for the wave's 16 columns; fv: V along the tokens
-template <typename T, int DK>
+// acc (the start state's part) += P V for 16 columns from c0 on of a V tile VD wide; fv: V along
+// the tokens
+template <typename T, int VD, bool LEAN = false>
 __device__ __forceinline__ void add_intra(f32x4_t (&acc)[4], const Frag<T> (&fv)[2], const char* sP, const char* sV,
-                                          int wave, int lane) {
+                                          int c0, int lane) {
   const int g = lane >> 4, n = lane & 15;
+  const uint32_t cb = col_base<T, LEAN>(lane);
   f32x4_t a[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
@@ -472,7 +516,7 @@ __device__ __forceinline__ void add_intra(f32x4_t (&acc)[4], const Frag<T> (&fv)
 #pragma unroll
     for (int s = 0; s <= t / 2; ++s) {
       Frag<T> fp;
-      col_frag<T>(fp, sP, 16 * t + n, s, g);
+      col_frag<T>(fp, sP, cb, 16 * t, s);
       mma(a[t], fv[s], fp);
     }
   }
@@ -488,7 +532,7 @@ __device__ __forceinline__ void add_intra(f32x4_t (&acc)[4], const Frag<T> (&fv)
       for (int j = 0; j <= 16 * t + n; ++j) {
         const float pj = Elem<T>::load(sP + Tile<T, 64>::quad(16 * t + n, j >> 2), j & 3);
         float x[4];
-        ld_quad<T>(sV + Tile<T, VT>::quad(j, 4 * wave + g), 0, x);
+        ld_quad<T>(sV + Tile<T, VD>::quad(j, c0 / 4 + g), 0, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[t][i] = fmaf(pj, x[i], a[t][i]);
       }
@@ -499,10 +543,11 @@ __device__ __forceinline__ void add_intra(f32x4_t (&acc)[4], const Frag<T> (&fv)
 }
 
 // S <- decay S + K^T (col o V); EXACT: the weighted values in three bf16 terms instead of two
-template <typename T, int DK, bool EXACT>
+template <typename T, int DK, bool EXACT, bool LEAN = false>
 __device__ __forceinline__ void add_chunk(f32x4_t (&S)[DK / 16], const Frag<T> (&fv)[2], const char* sK,
                                           const Decays& dc, int lane) {
   const int g = lane >> 4;
+  const uint32_t tb = tok_base<T, DK, LEAN>(lane);
   const float tot = dc.tot;
 #pragma unroll
   for (int ct = 0; ct < DK / 16; ++ct)
@@ -527,7 +572,7 @@ __device__ __forceinline__ void add_chunk(f32x4_t (&S)[DK / 16], const Frag<T> (
 #pragma unroll
     for (int ct = 0; ct < DK / 16; ++ct) {
       Frag<T> fk;
-      tok_frag<T, DK>(fk, sK, 16 * ct, s, lane);
+      tok_frag<T, DK>(fk, sK, tb, 16 * ct, s, lane);
       mma(S[ct], fk, fh);
       if constexpr (sizeof(T) == 2) mma(S[ct], fk, fm);
       if constexpr (sizeof(T) == 2 && EXACT) mma(S[ct], fk, fl);
@@ -536,14 +581,15 @@ __device__ __forceinline__ void add_chunk(f32x4_t (&S)[DK / 16], const Frag<T> (
 }
 
 // acc to the outputs of chunk c
-template <typename T, bool REV>
+template <typename T, bool REV, bool LEAN = false>
 __device__ __forceinline__ void store_out(const f32x4_t (&acc)[4], const LinaWalk& w, const Chain& ch, int c, int wave,
                                           int lane) {
   const int g = lane >> 4, n = lane & 15;
   const int64_t t0 = ch.lo + (int64_t)c * C;
   const uint32_t ro = w.H * w.dv, have = ch.rows(c);
   const size_t at = ((size_t)t0 * w.H + ch.h) * w.dv + ch.vt * VT;
-  auto off = [&](int t) { return (REV ? C - 1 - (16 * t + n) : 16 * t + n) * ro + 16 * wave + 4 * g; };
+  const uint32_t o = fresh<LEAN>(row_off(REV, n, ro) + 16 * wave + 4 * g);
+  auto off = [&](int t) { return o + rows_off(REV, 16 * t, ro); };
   if (sizeof(T) == 2 && !w.out_f32) {
     const Rows b((char*)w.out + at * 2, have * ro * 2);
 #pragma unroll
@@ -561,10 +607,10 @@ template <typename T>
 struct DotRows {
   u32x4_t r[4];
   __device__ __forceinline__ void load(const Rows& b, uint32_t step, bool rev, int wave, int lane) {
+    const uint32_t o = (row_off(rev, lane & 15, step) + (16 * wave + 4 * (lane >> 4)) * (uint32_t)sizeof(T));
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int row = 16 * t + (lane & 15);
-      const uint32_t off = (rev ? C - 1 - row : row) * step + (16 * wave + 4 * (lane >> 4)) * (uint32_t)sizeof(T);
+      const uint32_t off = o + rows_off(rev, 16 * t, step);
       if constexpr (sizeof(T) == 2) {
         const u32x2_t x = b.load8(off);
         r[t][0] = x[0];
@@ -640,7 +686,7 @@ __device__ __forceinline__ void scale_rows(f32x4_t (&acc)[4], const Decays& dc, 
 // one wave: the chunk's per-token dots, from the four waves' parts
 template <int DOT, bool REV>
 __device__ __forceinline__ void store_dots(const WalkParams& p, const Chain& ch, int c, const float (&s)[4][C],
-                                           const float (&own)[C], int lane) {
+                                           const float* own, int lane) {
   float d;
   if constexpr (DOT == kDotRow) {
     d = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
