@@ -224,7 +224,6 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
     const Operand<T> v(w.x, w, ch.h, D, 0), u(w.v, w, ch.h, D, 0);
     Stage<T, D, true> rv, ru;
     float lg = 0.f;
-    const bool sums = WANT && ch.vt == 0;  // the scores are whole: one workgroup's sums of M do
     auto fetch = [&](int it) {
       const int c = chunk(it);
       const int64_t t = ch.lo + (int64_t)c * C;
@@ -266,7 +265,7 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
           }
           const float4 jh = *(const float4*)&dc.hi[16 * J + 4 * g], jl = *(const float4*)&dc.lo[16 * J + 4 * g];
           const float jhs[4] = {jh.x, jh.y, jh.z, jh.w}, jls[4] = {jl.x, jl.y, jl.z, jl.w};
-          float m[4];
+          float m[4], cols = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = 16 * J + 4 * g + i;
@@ -275,19 +274,18 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
             y[i] = j <= row ? b[i] * r : 0.f;
             m[i] = j < row ? (a[i] * r) * b[i] : 0.f;
           }
-          if (sums) {
+          if (WANT && (p.k.nv == 1 || ((wave + J) & 1) == ch.vt)) {  // M is whole: half of its tiles here
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              own += m[i];
-              m[i] = row16_sum(m[i]);
-            }
-            if (n == 0) *(float4*)&scol[wave][16 * J + 4 * g] = make_float4(m[0], m[1], m[2], m[3]);
+            for (int i = 0; i < 4; ++i) own += m[i];
+            cols = row16_sums(m, n);
           }
+          if constexpr (WANT)
+            if (n < 4) scol[wave][16 * J + 4 * g + n] = cols;
         }
         pk[J] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         pv[J] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
       }
-      if (sums) {
+      if constexpr (WANT) {
         own += __shfl_xor(own, 16);
         own += __shfl_xor(own, 32);
         if (g == 0) sown[row] = own;
@@ -309,7 +307,7 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
           *(uint2*)(smem + Lds::PV + at) = pv[J];
         }
       if constexpr (WANT)
-        if (sums && wave == 0) store_dots<kDotCross, true>(p.v, ch, chunk(it), scol, sown, lane);
+        if (wave == 0) store_dots<kDotCross, true>(p.v, ch, chunk(it), scol, sown, lane);
       if (it + 1 < steps) put(it + 1);
       if (it + 2 < steps) fetch(it + 2);
       lds_barrier();

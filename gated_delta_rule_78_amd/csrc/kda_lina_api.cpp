@@ -318,7 +318,7 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
   }
   if (!(toks > 0 && fused) && kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
   if (p.dg && toks > 0 &&
-      kda::launch_lina_ddecay(w, da, db, de, s.dk / 64, fused ? 1 : s.dv / 64, anchor, p.per_head ? nullptr : p.dg,
+      kda::launch_lina_ddecay(w, da, db, de, s.dk / 64, s.dv / 64, anchor, p.per_head ? nullptr : p.dg,
                               (double*)(ws + l.off_part), p.per_head ? p.dg : nullptr) != hipSuccess)
     return KDA_ERR_HIP;
   return KDA_OK;

@@ -181,15 +181,20 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
 #endif
 }
 
-// sum over the 16 lanes of a DPP row, in every lane
-__device__ __forceinline__ float row16_sum(float x) {
-#define KDA_ROR(n) x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + n, 0xF, 0xF, true))
-  KDA_ROR(8);
-  KDA_ROR(4);
-  KDA_ROR(2);
-  KDA_ROR(1);
-#undef KDA_ROR
-  return x;
+// Sums of four values over the 16 lanes of a DPP row: lane n gets that of value n % 4.  Two values
+// share each step until one is left, then the row's quads are added: eleven operations for four.
+__device__ __forceinline__ float row16_sums(const float (&v)[4], int n) {
+#define KDA_DPP(x, ctrl) __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xF, 0xF, true))
+  const bool odd = n & 1, up = n & 2;
+  const float a0 = odd ? v[1] : v[0], b0 = odd ? v[0] : v[1];
+  const float a1 = odd ? v[3] : v[2], b1 = odd ? v[2] : v[3];
+  const float x = a0 + KDA_DPP(b0, 0xB1), y = a1 + KDA_DPP(b1, 0xB1);  // with lane n ^ 1
+  const float a = up ? y : x, b = up ? x : y;
+  float s = a + KDA_DPP(b, 0x4E);                                      // with lane n ^ 2
+  s += KDA_DPP(s, 0x124);                                              // the row's quads, rotated
+  s += KDA_DPP(s, 0x128);
+#undef KDA_DPP
+  return s;
 }
 
 // hi and residual of eight values as bf16 fragments
@@ -450,17 +455,20 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
       }
       const float4 jh = *(const float4*)&dc.hi[16 * J + 4 * g], jl = *(const float4*)&dc.lo[16 * J + 4 * g];
       const float jhs[4] = {jh.x, jh.y, jh.z, jh.w}, jls[4] = {jl.x, jl.y, jl.z, jl.w};
+      float m[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = 16 * J + 4 * g + i;
         const float r = a[i] * fast_exp2((ih - jhs[i]) + (il - jls[i]));
         x[i] = j <= row ? r : 0.f;
         if constexpr (DOT == kDotCross) {
-          const float m = j < row ? r * e[i] : 0.f;
-          own_sum += m;
-          const float cs = row16_sum(m);
-          if (n == 0) cols[j] = cs;
+          m[i] = j < row ? r * e[i] : 0.f;
+          own_sum += m[i];
         }
+      }
+      if constexpr (DOT == kDotCross) {
+        const float cs = row16_sums(m, n);
+        if (n < 4) cols[16 * J + 4 * g + n] = cs;
       }
     }
     if (J <= (wave | 1)) st_quad<T>(sP + 16 * wave * Tile<T, 64>::RB + (vb ^ (J * 16 * sizeof(T))), x);
