@@ -27,12 +27,13 @@
 // token and stores them at once; K and V are read along the token axis with the LDS
 // transpose loads.
 //
-// Precision (bf16 inputs): sums, decays and the state are fp32.  Rounded to bf16 (off by at most
-// 2^-8 relative, as the output itself is) are P = r o QK^T and the state where it is multiplied
-// by q.  What enters the fp32 state, e^{G_C - G_j} v_j, goes through the matrix cores as a bf16
-// pair (value and residual, 2^-16); in the walks that a and b are taken from, it and the state
-// where it meets the row go as three bf16 terms (2^-24): D is a small difference of long sums
-// of a and b, and with pairs its error was 1e-5 of the gradient's norm, now 6e-7.
+// Precision (bf16 inputs): sums, decays and the state are fp32, and what enters the state,
+// e^{G_C - G_j} v_j, goes through the matrix cores as three bf16 terms, all of its 24 bits (two
+// terms left the state 2.4e-6 of its norm off, three 2e-7, as fp32 sums do; a sixth more matrix
+// work).  Rounded to bf16 (off by at most 2^-8 relative, as the output itself is) are P = r o QK^T
+// and the state where it is multiplied by q.  In the walks that a and b are taken from, the state
+// meets its rows as three terms too: D is a small difference of long sums of a and b, and with
+// two-term operands its error was 1e-5 of the gradient's norm, now 6e-7.
 #include <type_traits>
 
 #include "kda_lina_tile.h"
@@ -172,7 +173,7 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       tok_frag<T, VT>(fv[1], tV(it), tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
       add_intra<T, VT>(acc, fv, tP(it), tV(it), 16 * wave, lane);
       store_out<T, REV>(acc, w, ch, c, wave, lane);
-      add_chunk<T, DK, DOT == kDotRow>(S, fv, tK(it), dc, lane);
+      add_chunk<T, DK>(S, fv, tK(it), dc, lane);
       if constexpr (DOT == kDotRow && REV)
         if (c % kLinaGroup == 0) store_anchor<DK>(p, ch, c, tid, S);
       lds_barrier();
@@ -357,7 +358,7 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
       lds_barrier();
       add_intra<T, D, true>(acc, fv, smem + tp, tile(it, tv), c0, lane);
       store_out<T, true, true>(acc, wp.w, ch, c, wave, lane);
-      add_chunk<T, D, EXACT, true>(S, fv, tile(it, tk), dc, lane);
+      add_chunk<T, D, true>(S, fv, tile(it, tk), dc, lane);
       if constexpr (EXACT)
         if (c % kLinaGroup == 0) store_anchor<D>(wp, ch, c, tid, S);
       lds_barrier();
@@ -462,7 +463,7 @@ __global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
     tok_frag<T, VT>(fv[1], sV, tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
     add_intra<T, VT>(acc, fv, sP, sV, 16 * wave, lane);
     store_out<T, REV>(acc, w, ch, c, wave, lane);
-    add_chunk<T, DK, false>(S, fv, sK, dc, lane);
+    add_chunk<T, DK>(S, fv, sK, dc, lane);
     if constexpr (DOT == kDotRow && REV)
       if (c % kLinaGroup == 0) store_anchor<DK>(p, ch, c, tid, S);
   }
@@ -471,7 +472,7 @@ __global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
 
 // End states of the segments from a zero start: the walk without its outputs.  Two tile
 // buffers, one barrier per chunk; small enough for three workgroups on a compute unit.
-template <typename T, int DK, bool REV, bool EXACT>
+template <typename T, int DK, bool REV>
 __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
   constexpr int TILES = Tile<T, DK>::BYTES + Tile<T, VT>::BYTES;
   extern __shared__ __align__(16) char smem[];
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
     tok_frag<T, VT>(fv[0], t + Tile<T, DK>::BYTES, tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
     tok_frag<T, VT>(fv[1], t + Tile<T, DK>::BYTES, tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
     total *= dc.tot;
-    add_chunk<T, DK, EXACT>(S, fv, t, dc, lane);
+    add_chunk<T, DK>(S, fv, t, dc, lane);
     lds_barrier();
   }
   f32x4_t* to = (f32x4_t*)(w.seg_state + ch.at(p, ch.seg) * (DK * VT));
@@ -574,12 +575,8 @@ hipError_t walk_f32(const WalkParams& p) {
 template <typename T, int DK>
 hipError_t segments(const WalkParams& p) {
   const int lds = 2 * (Tile<T, DK>::BYTES + Tile<T, VT>::BYTES);
-  const bool exact = sizeof(T) == 2 && p.w.dot == kDotRow;
-  if (p.w.rev)
-    return exact ? launch(lina_segment_kernel<T, DK, true, true>, p, NT, lds)
-                 : launch(lina_segment_kernel<T, DK, true, false>, p, NT, lds);
-  return exact ? launch(lina_segment_kernel<T, DK, false, true>, p, NT, lds)
-               : launch(lina_segment_kernel<T, DK, false, false>, p, NT, lds);
+  return p.w.rev ? launch(lina_segment_kernel<T, DK, true>, p, NT, lds)
+                 : launch(lina_segment_kernel<T, DK, false>, p, NT, lds);
 }
 
 // Packed offsets clamped to [0, T] and made non-decreasing (a running maximum), cs[0] = 0, and

@@ -197,17 +197,6 @@ __device__ __forceinline__ float row16_sums(const float (&v)[4], int n) {
   return s;
 }
 
-// hi and residual of eight values as bf16 fragments
-__device__ __forceinline__ void split_pair(const float (&x)[8], Frag<bf16_t>& hi, Frag<bf16_t>& lo) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i], b = x[2 * i + 1];
-    const uint32_t h = pack_bf16x2(a, b);
-    hi.w[i] = h;
-    lo.w[i] = pack_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xFFFF0000u));
-  }
-}
-
 // three bf16 terms: all 24 bits
 __device__ __forceinline__ void split_triple(const float (&x)[8], Frag<bf16_t>& hi, Frag<bf16_t>& mid,
                                              Frag<bf16_t>& lo) {
@@ -498,13 +487,17 @@ __device__ __forceinline__ void from_state(const f32x4_t (&S)[DK / 16], const ch
       fs.from_acc(S[2 * s], S[2 * s + 1]);
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      Frag<T> fq;
-      row_frag<T, DK>(fq, sQ, rb, 16 * t, s);
-      mma(acc[t], fs, fq);
+    for (int t2 = 0; t2 < 4; t2 += 2) {
+      Frag<T> fq[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) row_frag<T, DK>(fq[x], sQ, rb, 16 * (t2 + x), s);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) mma(acc[t2 + x], fs, fq[x]);
       if constexpr (sizeof(T) == 2 && EXACT) {
-        mma(acc[t], fm, fq);
-        mma(acc[t], fl, fq);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) mma(acc[t2 + x], fm, fq[x]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) mma(acc[t2 + x], fl, fq[x]);
       }
     }
   }
@@ -550,8 +543,8 @@ __device__ __forceinline__ void add_intra(f32x4_t (&acc)[4], const Frag<T> (&fv)
   for (int t = 0; t < 4; ++t) acc[t] = a[t];
 }
 
-// S <- decay S + K^T (col o V); EXACT: the weighted values in three bf16 terms instead of two
-template <typename T, int DK, bool EXACT, bool LEAN = false>
+// S <- decay S + K^T (col o V), the weighted values in three bf16 terms
+template <typename T, int DK, bool LEAN = false>
 __device__ __forceinline__ void add_chunk(f32x4_t (&S)[DK / 16], const Frag<T> (&fv)[2], const char* sK,
                                           const Decays& dc, int lane) {
   const int g = lane >> 4;
@@ -572,18 +565,22 @@ __device__ __forceinline__ void add_chunk(f32x4_t (&S)[DK / 16], const Frag<T> (
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) fh.w[e] = x[e];
-    } else if constexpr (EXACT) {
-      split_triple(x, fh, fm, fl);
     } else {
-      split_pair(x, fh, fm);
+      split_triple(x, fh, fm, fl);
     }
 #pragma unroll
-    for (int ct = 0; ct < DK / 16; ++ct) {
-      Frag<T> fk;
-      tok_frag<T, DK>(fk, sK, tb, 16 * ct, s, lane);
-      mma(S[ct], fk, fh);
-      if constexpr (sizeof(T) == 2) mma(S[ct], fk, fm);
-      if constexpr (sizeof(T) == 2 && EXACT) mma(S[ct], fk, fl);
+    for (int c2 = 0; c2 < DK / 16; c2 += 2) {  // two tiles in turn: a product waits for the last on its tile
+      Frag<T> fk[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) tok_frag<T, DK>(fk[x], sK, tb, 16 * (c2 + x), s, lane);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) mma(S[c2 + x], fk[x], fh);
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) mma(S[c2 + x], fk[x], fm);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) mma(S[c2 + x], fk[x], fl);
+      }
     }
   }
 }
