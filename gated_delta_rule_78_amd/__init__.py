@@ -197,6 +197,27 @@ def _stream(dev):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _launch(entry, dev, *args):
+    """Calls an entry point with the current stream of `dev`, on that device; raises on a status.
+    Pointers are passed as integers (0: NULL)."""
+    import torch
+    f = getattr(_lib or lib(), entry)
+    # the raw stream without a Stream object around it, which takes longer than the call
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    stream = raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, stream)
+    if rc != 0:
+        raise KdaError(rc, entry)
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
 def workspace_size(B, T, H, dk, dv, dtype="bf16") -> int:
     """Bytes of device workspace the two-pass chunk forward needs for this shape."""
     shape = Shape(B, T, H, dk, dv, 64, BF16 if dtype == "bf16" else F32)
@@ -264,15 +285,23 @@ def _chunk_call(debug, q, k, v, alpha, beta, initial_state, out, final_state, wa
     return out, final_state, dbg
 
 
+def _prepared(q, k, qk_prep):
+    """q and k as the kernels take them: as they are, or through qk_norm_rope(**qk_prep)."""
+    return (q, k) if qk_prep is None else qk_norm_rope(q, k, **qk_prep)
+
+
 def chunk_fwd(q, k, v, alpha, beta, initial_state=None, out=None, final_state=None, want_final=True,
-              path="auto", workspace=None):
+              path="auto", workspace=None, qk_prep=None):
     """Chunkwise WY forward.  q, k, alpha [B,T,H,dk]; v [B,T,H,dv]; beta [B,T,H]
     (all bf16 or all fp32, contiguous, on one GPU); initial_state fp32 [B,H,dk,dv]
     or None.  path: "fused" (single pass), "twopass" (parallel per-chunk records in a
     workspace, then the state pass), "capi" (kda_chunk_fwd's own choice, with its
     workspace from the stream-ordered pool) or "auto".  workspace: optional uint8 device
     tensor of at least workspace_size(...) bytes for the two-pass path (allocated
-    here when omitted).  Returns (o [B,T,H,dv], final_state fp32 [B,H,dk,dv] or None)."""
+    here when omitted).  qk_prep: keyword arguments of qk_norm_rope, with which q and k are
+    prepared first (the rule asks for unit keys: dict(norm="l2")); None takes them as they are.
+    Returns (o [B,T,H,dv], final_state fp32 [B,H,dk,dv] or None)."""
+    q, k = _prepared(q, k, qk_prep)
     o, s, _ = _chunk_call(False, q, k, v, alpha, beta, initial_state, out, final_state, want_final, path,
                           workspace)
     return o, s
@@ -371,10 +400,12 @@ def chunk_fwd_debug(q, k, v, alpha, beta, initial_state=None):
     return _chunk_call(True, q, k, v, alpha, beta, initial_state, None, None, True)
 
 
-def decode_step(q, k, v, alpha, beta, state, out=None, _entry="kda_decode_step"):
+def decode_step(q, k, v, alpha, beta, state, out=None, _entry="kda_decode_step", qk_prep=None):
     """One recurrent token for every (b, h).  q, k, alpha [B,H,dk]; v [B,H,dv];
-    beta [B,H]; state fp32 [B,H,dk,dv] updated in place.  Returns o [B,H,dv]."""
+    beta [B,H]; state fp32 [B,H,dk,dv] updated in place; qk_prep as chunk_fwd.
+    Returns o [B,H,dv]."""
     torch = _torch()
+    q, k = _prepared(q, k, qk_prep)
     B, H, dk = q.shape
     dv = v.shape[-1]
     code = _dtype_code(q)
@@ -498,13 +529,14 @@ def gdn2_decode_tokens(q, k, v, alpha, erase, write, state, out=None):
 
 
 def chunk_fwd_varlen(q, k, v, alpha, beta, cu_seqlens, initial_state=None, out=None, final_state=None,
-                     want_final=True, workspace=None, erase=None, write=None, sfda=False):
+                     want_final=True, workspace=None, erase=None, write=None, sfda=False, qk_prep=None):
     """Packed variable-length batch: q, k, alpha [1,T,H,dk]; v [1,T,H,dv]; beta [1,T,H]
     (or, for Gated DeltaNet-2, beta=None with erase [1,T,H,dk] and write [1,T,H,dv];
     sfda=True: alpha holds the SFDA complex gates); cu_seqlens int32 [N+1] on the
-    device; states [N,H,dk,dv] fp32.
+    device; states [N,H,dk,dv] fp32; qk_prep as chunk_fwd.
     Returns (o [1,T,H,dv], final_state [N,H,dk,dv] or None)."""
     torch = _torch()
+    q, k = _prepared(q, k, qk_prep)
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     if B != 1:

@@ -9,8 +9,24 @@ states have the same layout.  As everywhere here, nothing is normalised or scale
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import gated_delta_rule_78_amd as _kda
+
+
+@functools.lru_cache(maxsize=1024)
+def _sized(B, T, Hk, H, dk, dv, code, n, bwd):
+    """(the C shape, bytes of workspace); n: sequences of a packed batch, or -1."""
+    shape = _kda.Shape(B, T, H, dk, dv, 64, code)
+    ref = ctypes.byref(shape)
+    L = _kda.lib()
+    if bwd:
+        need = L.kda_lina_chunk_bwd_workspace_size(ref, Hk) if n < 0 else \
+            L.kda_lina_chunk_bwd_varlen_workspace_size(ref, Hk, n)
+    else:
+        need = L.kda_lina_chunk_fwd_workspace_size(ref) if n < 0 else \
+            L.kda_lina_chunk_fwd_varlen_workspace_size(ref, n)
+    return shape, int(need)
 
 
 def _operands(q, k, v, log_decay, lead):
@@ -55,20 +71,22 @@ def _packed(cu_seqlens, B):
 
 def _workspace(need, workspace, dev):
     torch = _kda._torch()
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    return workspace, ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def lina_chunk_fwd(q, k, v, log_decay, initial_state=None, out=None, final_state=None, want_final=True,
-                   cu_seqlens=None, workspace=None):
+                   cu_seqlens=None, workspace=None, qk_prep=None):
     """Chunked forward over whole sequences.  q, k [B,T,Hk,dk] and v [B,T,H,dv] (all bf16 or all
     fp32, contiguous; Hk divides H, head h of v goes with head h // (H // Hk) of q and k);
     log_decay fp32 [B,T,H], or [H] for a fixed decay per head; initial_state fp32 [B,H,dk,dv] or
     None.  cu_seqlens (int32 [N+1] on the device): a packed batch, B == 1, states [N,H,dk,dv];
-    tokens after the last offset are not written.  Returns (o [B,T,H,dv], final_state fp32 or
+    tokens after the last offset are not written.  qk_prep: keyword arguments of qk_norm_rope, with
+    which q and k are prepared first, or None.  Returns (o [B,T,H,dv], final_state fp32 or
     None)."""
     torch = _kda._torch()
+    q, k = _kda._prepared(q, k, qk_prep)
     B, T = q.shape[:2]
     Hk, H, dk, dv, code, per_head = _operands(q, k, v, log_decay, (B, T))
     n = _packed(cu_seqlens, B)
@@ -80,26 +98,16 @@ def lina_chunk_fwd(q, k, v, log_decay, initial_state=None, out=None, final_state
     if final_state is None and want_final:
         final_state = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
     _states(((initial_state, "initial_state"), (final_state, "final_state")), n, H, dk, dv)
-    shape = _kda.Shape(B, T, H, dk, dv, 64, code)
-    L = _kda.lib()
-    if cu_seqlens is None:
-        need = int(L.kda_lina_chunk_fwd_workspace_size(ctypes.byref(shape)))
-    else:
-        need = int(L.kda_lina_chunk_fwd_varlen_workspace_size(ctypes.byref(shape), n))
+    shape, need = _sized(B, T, Hk, H, dk, dv, code, -1 if cu_seqlens is None else n, False)
     workspace, nbytes = _workspace(need, workspace, dev)
-    p = _kda._ptr
     _kda._check((q, k, v, log_decay, cu_seqlens, initial_state, out, final_state, workspace),
                 ("q", "k", "v", "log_decay", "cu_seqlens", "initial_state", "out", "final_state", "workspace"), dev)
-    args = (p(q), p(k), p(v), p(log_decay), int(per_head), p(initial_state), p(out), p(final_state), p(workspace),
-            nbytes, _kda._stream(dev))
-    with torch.cuda.device(dev):
-        if cu_seqlens is None:
-            rc, where = L.kda_lina_chunk_fwd(ctypes.byref(shape), Hk, *args), "kda_lina_chunk_fwd"
-        else:
-            rc = L.kda_lina_chunk_fwd_varlen(ctypes.byref(shape), Hk, p(cu_seqlens), n, *args)
-            where = "kda_lina_chunk_fwd_varlen"
-    if rc != 0:
-        raise _kda.KdaError(rc, where)
+    p = _kda._addr
+    args = (p(q), p(k), p(v), p(log_decay), per_head, p(initial_state), p(out), p(final_state), p(workspace), nbytes)
+    if cu_seqlens is None:
+        _kda._launch("kda_lina_chunk_fwd", dev, ctypes.byref(shape), Hk, *args)
+    else:
+        _kda._launch("kda_lina_chunk_fwd_varlen", dev, ctypes.byref(shape), Hk, p(cu_seqlens), n, *args)
     return out, final_state
 
 
@@ -123,26 +131,17 @@ def lina_chunk_bwd(q, k, v, log_decay, d_o, initial_state=None, d_final_state=No
     gq, gk, gv = new(q), new(k), new(v)
     gd = new(log_decay) if want_d_decay else None
     gs = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev) if want_d_initial else None
-    shape = _kda.Shape(B, T, H, dk, dv, 64, code)
-    L = _kda.lib()
-    if cu_seqlens is None:
-        need = int(L.kda_lina_chunk_bwd_workspace_size(ctypes.byref(shape), Hk))
-    else:
-        need = int(L.kda_lina_chunk_bwd_varlen_workspace_size(ctypes.byref(shape), Hk, n))
+    shape, need = _sized(B, T, Hk, H, dk, dv, code, -1 if cu_seqlens is None else n, True)
     workspace, nbytes = _workspace(need, workspace, dev)
-    p = _kda._ptr
     _kda._check((q, k, v, log_decay, d_o, cu_seqlens, initial_state, d_final_state, workspace),
                 ("q", "k", "v", "log_decay", "d_o", "cu_seqlens", "initial_state", "d_final_state", "workspace"), dev)
-    args = (p(q), p(k), p(v), p(log_decay), int(per_head), p(initial_state), p(d_o), p(d_final_state), p(gq), p(gk),
-            p(gv), p(gd), p(gs), p(workspace), nbytes, _kda._stream(dev))
-    with torch.cuda.device(dev):
-        if cu_seqlens is None:
-            rc, where = L.kda_lina_chunk_bwd(ctypes.byref(shape), Hk, *args), "kda_lina_chunk_bwd"
-        else:
-            rc = L.kda_lina_chunk_bwd_varlen(ctypes.byref(shape), Hk, p(cu_seqlens), n, *args)
-            where = "kda_lina_chunk_bwd_varlen"
-    if rc != 0:
-        raise _kda.KdaError(rc, where)
+    p = _kda._addr
+    args = (p(q), p(k), p(v), p(log_decay), per_head, p(initial_state), p(d_o), p(d_final_state), p(gq), p(gk), p(gv),
+            p(gd), p(gs), p(workspace), nbytes)
+    if cu_seqlens is None:
+        _kda._launch("kda_lina_chunk_bwd", dev, ctypes.byref(shape), Hk, *args)
+    else:
+        _kda._launch("kda_lina_chunk_bwd_varlen", dev, ctypes.byref(shape), Hk, p(cu_seqlens), n, *args)
     return gq, gk, gv, gd, gs
 
 
@@ -156,25 +155,23 @@ def _decode(entry, q, k, v, log_decay, state, out, lead):
         out = torch.empty_like(v)
     elif out.dtype != q.dtype or out.shape != v.shape:
         raise ValueError("out must have the shape of v and the dtype of q")
-    p = _kda._ptr
     _kda._check((q, k, v, log_decay, state, out), ("q", "k", "v", "log_decay", "state", "out"), dev)
-    shape = _kda.Shape(B, T, H, dk, dv, 0, code)
-    with torch.cuda.device(dev):
-        rc = getattr(_kda.lib(), entry)(ctypes.byref(shape), Hk, p(q), p(k), p(v), p(log_decay), int(per_head),
-                                        p(state), p(out), _kda._stream(dev))
-    if rc != 0:
-        raise _kda.KdaError(rc, entry)
+    p = _kda._addr
+    shape, _ = _sized(B, T, Hk, H, dk, dv, code, -1, False)
+    _kda._launch(entry, dev, ctypes.byref(shape), Hk, p(q), p(k), p(v), p(log_decay), per_head, p(state), p(out))
     return out
 
 
-def lina_decode_step(q, k, v, log_decay, state, out=None):
+def lina_decode_step(q, k, v, log_decay, state, out=None, qk_prep=None):
     """One recurrent token for every (b, h): q, k [B,Hk,dk]; v [B,H,dv]; log_decay fp32 [B,H] or
-    [H]; state fp32 [B,H,dk,dv] updated in place.  Returns o [B,H,dv]."""
+    [H]; state fp32 [B,H,dk,dv] updated in place; qk_prep as lina_chunk_fwd.  Returns o [B,H,dv]."""
+    q, k = _kda._prepared(q, k, qk_prep)
     return _decode("kda_lina_decode_step", q, k, v, log_decay, state, out, tuple(q.shape[:1]))
 
 
-def lina_decode_tokens(q, k, v, log_decay, state, out=None):
+def lina_decode_tokens(q, k, v, log_decay, state, out=None, qk_prep=None):
     """Several tokens per (b, h) with the state read and written once: q, k [B,T,Hk,dk];
     v [B,T,H,dv]; log_decay fp32 [B,T,H] or [H]; state fp32 [B,H,dk,dv] in place.
-    Returns o [B,T,H,dv]."""
+    qk_prep as lina_chunk_fwd.  Returns o [B,T,H,dv]."""
+    q, k = _kda._prepared(q, k, qk_prep)
     return _decode("kda_lina_decode_tokens", q, k, v, log_decay, state, out, tuple(q.shape[:2]))

@@ -29,10 +29,11 @@ def _tokens(x, nm, dev):
     """(stride between tokens, dense) of [B,T,H,d] or [B,H,d] whose rows of a token are dense."""
     if not x.is_cuda or x.device != dev:
         raise ValueError(f"{nm} must be on {dev}")
-    *lead, H, d = x.shape
+    H, d = x.shape[-2:]
     dense = H * d
-    if 0 in x.shape:
+    if x.is_contiguous():
         return dense, True
+    lead = x.shape[:-2]
     if x.stride(-1) != 1 or (H > 1 and x.stride(-2) != d):
         raise ValueError(f"{nm}: the heads of a token must lie back to back")
     step = None
@@ -64,9 +65,7 @@ def _shape(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interl
         if k.dim() != q.dim() or tuple(k.shape[:-2]) != lead or k.shape[-1] != d:
             raise ValueError("shapes: q [..., Hq, d]; k [..., Hk, d]")
     dev = q.device
-    n = 1
-    for x in lead:
-        n *= x
+    n = lead[0] if len(lead) == 1 else lead[0] * lead[1]
     s = _kda.QkShape(tokens=n, q_heads=Hq, k_heads=0 if k is None else k.shape[-2], d=d, norm=_NORMS[norm],
                      eps=float(eps), weight_offset=float(weight_offset), interleaved=int(bool(interleaved)),
                      dtype=_kda._dtype_code(q))
@@ -108,7 +107,7 @@ def _like(out, x, nm, dev):
     if x is None:
         return None
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=dev)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
     if out.dtype != x.dtype or out.shape != x.shape:
         raise ValueError(f"{nm} must have the shape and dtype of its input")
     _kda._check((out,), (nm,), dev)
@@ -130,12 +129,9 @@ def qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps=1e-
     s, dev, _, _ = _shape(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interleaved)
     _weights(((q_weight, "q_weight"), (k_weight, "k_weight")), q.shape[-1], dev)
     q_out, k_out = _like(q_out, q, "q_out", dev), _like(k_out, k, "k_out", dev)
-    p = _kda._ptr
-    with _kda._torch().cuda.device(dev):
-        rc = _kda.lib().kda_qk_norm_rope(ctypes.byref(s), p(q), p(k), p(q_weight), p(k_weight), p(inv_freq),
-                                         p(positions), p(q_out), p(k_out), _kda._stream(dev))
-    if rc != 0:
-        raise _kda.KdaError(rc, "kda_qk_norm_rope")
+    p = _kda._addr
+    _kda._launch("kda_qk_norm_rope", dev, ctypes.byref(s), p(q), p(k), p(q_weight), p(k_weight), p(inv_freq),
+                 p(positions), p(q_out), p(k_out))
     return q_out, k_out
 
 
@@ -163,11 +159,7 @@ def qk_norm_rope_bwd(d_q, d_k, q, k=None, *, norm="rms", q_weight=None, k_weight
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _kda._check((workspace,), ("workspace",), dev)
-    p = _kda._ptr
-    with torch.cuda.device(dev):
-        rc = _kda.lib().kda_qk_norm_rope_bwd(ctypes.byref(s), p(d_q), p(d_k), p(q), p(k), p(q_weight), p(k_weight),
-                                             p(inv_freq), p(positions), p(gq), p(gk), p(gwq), p(gwk), p(workspace),
-                                             ctypes.c_size_t(nbytes), _kda._stream(dev))
-    if rc != 0:
-        raise _kda.KdaError(rc, "kda_qk_norm_rope_bwd")
+    p = _kda._addr
+    _kda._launch("kda_qk_norm_rope_bwd", dev, ctypes.byref(s), p(d_q), p(d_k), p(q), p(k), p(q_weight), p(k_weight),
+                 p(inv_freq), p(positions), p(gq), p(gk), p(gwq), p(gwk), p(workspace), nbytes)
     return gq, gk, gwq, gwk

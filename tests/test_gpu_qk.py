@@ -308,3 +308,37 @@ def test_run_of_the_operators():
     beta = torch.full((B, T, Hq), 0.5, device="cuda", dtype=torch.bfloat16)
     od, _ = kda.chunk_fwd(qb, kb, vp[:, :, :Hq].contiguous().bfloat16(), one, beta)
     assert bool(torch.isfinite(od).all())
+
+
+def test_prepared_on_the_way_in():
+    """qk_prep of the forward and decode entry points equals preparing q and k before the call."""
+    import torch
+
+    import gated_delta_rule_78_amd as kda
+    B, T, H, d = 2, 70, 2, 128
+    qkv = _make(B, T, 3 * H, d, "bf16", 3)
+    q, k, v = qkv[:, :, :H], qkv[:, :, H:2 * H], qkv[:, :, 2 * H:].contiguous()
+    prep = dict(norm="l2", inv_freq=kda.rope_inv_freq(64), positions=torch.arange(T, device="cuda").repeat(B, 1))
+    qn, kn = kda.qk_norm_rope(q, k, **prep)
+    al = torch.rand(B, T, H, d, device="cuda").bfloat16()
+    be = torch.rand(B, T, H, device="cuda").bfloat16()
+    g = -torch.rand(B, T, H, device="cuda")
+    same = lambda a, b: all(torch.equal(x, y) for x, y in zip(a, b))
+    assert same(kda.chunk_fwd(q, k, v, al, be, qk_prep=prep), kda.chunk_fwd(qn, kn, v, al, be))
+    assert same(kda.lina_chunk_fwd(q, k, v, g, qk_prep=prep), kda.lina_chunk_fwd(qn, kn, v, g))
+    cu = torch.tensor([0, 50, B * T], dtype=torch.int32, device="cuda")
+    flat = lambda x: x.contiguous().reshape(1, B * T, *x.shape[2:])
+    one = dict(prep, positions=prep["positions"].reshape(1, B * T))
+    a = [flat(x) for x in (q, k, v, al, be)]
+    b = [flat(x) for x in (qn, kn, v, al, be)]
+    assert same(kda.chunk_fwd_varlen(*a, cu, qk_prep=one), kda.chunk_fwd_varlen(*b, cu))
+    S = torch.randn(B, H, d, d, device="cuda")
+    t = dict(prep, positions=prep["positions"][:, 5].contiguous())
+    at = lambda *xs: [x[:, 5].contiguous() for x in xs]
+    s1, s2 = S.clone(), S.clone()
+    assert torch.equal(kda.decode_step(*at(q, k, v, al, be), s1, qk_prep=t), kda.decode_step(*at(qn, kn, v, al, be), s2))
+    assert torch.equal(s1, s2)
+    s1, s2 = S.clone(), S.clone()
+    assert torch.equal(kda.lina_decode_step(*at(q, k, v, g), s1, qk_prep=t), kda.lina_decode_step(*at(qn, kn, v, g), s2))
+    assert torch.equal(kda.lina_decode_tokens(q, k, v, g, s1, qk_prep=prep), kda.lina_decode_tokens(qn, kn, v, g, s2))
+    assert torch.equal(s1, s2)
