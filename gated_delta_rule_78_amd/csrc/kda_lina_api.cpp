@@ -55,7 +55,9 @@ int segment_override() {
 // cost their successors a state to add, nch / L of them in a row: with a step of s and an
 // addition of f, 2 L s + f nch / L is least at L = sqrt(nch f / 2 s) (64 chunks of 8 chains: 30 us
 // at L = 3, 53 at 1, 63 at 16; fp32, 16 chunks: 25 us at 1, 45 at 4, 107 whole).  Packed chains
-// are dealt longest first, and cut only where one alone would outlast the others.
+// are dealt longest first; 256 or more are cut only where one alone would take twice as long as
+// all of them spread evenly (6 prompts of 20,011 tokens, H = 32: 241 us whole, 331 at L = 80; 24:
+// 217 and 262).
 Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   const bool packed = n_seqs >= 0;
   const int64_t nch = std::max<int64_t>(1, ((int64_t)s.T + 63) / 64);
@@ -65,7 +67,8 @@ Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   int64_t L = nch;
   if (packed || chains < 256) {
     L = (work + 255) / 256;
-    if (!packed && L >= 32) L = (work + 511) / 512;
+    if (chains >= 256) L *= 2;
+    else if (L >= 32) L = (work + 511) / 512;
     L = std::max<int64_t>(L, (int64_t)std::ceil(std::sqrt((double)nch * (s.dtype == KDA_BF16 ? 0.16 : 0.06))));
   }
   if (segment_override() > 0) L = segment_override();

@@ -215,7 +215,7 @@ def test_empty_batches():
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
-@pytest.mark.parametrize("B,T,decay", [(1, 1, "token"), (5, 3, "head"), (2, 17, "token")])
+@pytest.mark.parametrize("B,T,decay", [(1, 1, "token"), (5, 3, "head"), (2, 17, "token"), (700, 1, "head")])
 def test_decode(B, T, decay, dk, dv, dtype):
     """fp32 state and sums throughout: the state within fp32's bound, o rounded once more."""
     import torch
