@@ -246,8 +246,8 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
       const uint32_t rb = row_base<T, D, true>(lane);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        row_frag<T, D>(fv[s], tile(it, Lds::V), rb, 16 * wave, s);
-        row_frag<T, D>(fk[s], tile(it, Lds::K), rb, 16 * wave, s);
+        row_frag<T, D, true>(fv[s], tile(it, Lds::V), rb, 16 * wave, s);
+        row_frag<T, D, true>(fk[s], tile(it, Lds::K), rb, 16 * wave, s);
       }
       const float ih = dc.hi[row], il = dc.lo[row];
       float own = 0.f;
@@ -259,9 +259,9 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
             Frag<T> f;
-            row_frag<T, D>(f, tile(it, Lds::U), rb, 16 * J, s);
+            row_frag<T, D, true>(f, tile(it, Lds::U), rb, 16 * J, s);
             mma(a, f, fv[s]);
-            row_frag<T, D>(f, tile(it, Lds::Q), rb, 16 * J, s);
+            row_frag<T, D, true>(f, tile(it, Lds::Q), rb, 16 * J, s);
             mma(b, f, fk[s]);
           }
           const float4 jh = *(const float4*)&dc.hi[16 * J + 4 * g], jl = *(const float4*)&dc.lo[16 * J + 4 * g];

@@ -64,13 +64,29 @@ __device__ __forceinline__ uint32_t tok_base(int lane) {  // bf16: row 8 g + n /
   return sizeof(T) == 2 ? fresh<LEAN>(Tile<T, D>::quad(8 * g + (n >> 2), n & 3)) : 0;
 }
 
+// Addresses of two reads that must not be told to lie a constant apart: the compiler would make
+// one ds_read2st64_b64 of them, which takes 16 cycles where two ds_read_b64 take 5 (measured).
+template <bool LEAN>
+__device__ __forceinline__ uint32_t apart(uint32_t x) {
+#ifndef KDA_HOST_PASS
+  if constexpr (LEAN) asm volatile("" : "+v"(x));
+  else asm("" : "+v"(x));
+#endif
+  return x;
+}
+
 // row fragment of 32 columns: slots 0-3 columns 32 s + 4 g.., slots 4-7 columns 32 s + 16 + 4 g.. of
 // row r0 + n (r0 a multiple of 16): the order in which two 16-row accumulator tiles of the state
 // hold their rows
-template <typename T, int D>
+template <typename T, int D, bool LEAN = false>
 __device__ __forceinline__ void row_frag(Frag<T>& f, const char* t, uint32_t base, int r0, int s) {
-  const char* p = t + r0 * Tile<T, D>::RB;
-  f.load4x2(p + (base ^ (s * 32 * sizeof(T))), p + (base ^ ((s * 32 + 16) * sizeof(T))));
+  uint32_t a = (base ^ (s * 32 * sizeof(T))) + r0 * Tile<T, D>::RB;
+  uint32_t b = (base ^ ((s * 32 + 16) * sizeof(T))) + r0 * Tile<T, D>::RB;
+  if constexpr (sizeof(T) == 2) {
+    a = apart<LEAN>(a);
+    b = apart<LEAN>(b);
+  }
+  f.load4x2(t + a, t + b);
 }
 
 // token fragment: slots hold tokens 32 s + 8 g + e of column c0 + n (c0 a multiple of 16)
@@ -490,7 +506,7 @@ __device__ __forceinline__ void from_state(const f32x4_t (&S)[DK / 16], const ch
     for (int t2 = 0; t2 < 4; t2 += 2) {
       Frag<T> fq[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) row_frag<T, DK>(fq[x], sQ, rb, 16 * (t2 + x), s);
+      for (int x = 0; x < 2; ++x) row_frag<T, DK, LEAN>(fq[x], sQ, rb, 16 * (t2 + x), s);
 #pragma unroll
       for (int x = 0; x < 2; ++x) mma(acc[t2 + x], fs, fq[x]);
       if constexpr (sizeof(T) == 2 && EXACT) {
