@@ -244,10 +244,13 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
       const int row = 16 * wave + n;
       Frag<T> fv[KS], fk[KS];
       const uint32_t rb = row_base<T, D, true>(lane);
+      auto at = [&](int t, int r0) { return rows_at<T, D, true>(rb + t, r0); };
+      const uint32_t ov = at(Lds::V, 16 * wave), ok = at(Lds::K, 16 * wave);
+      const char* const t0 = tile(it, 0);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        row_frag<T, D, true>(fv[s], tile(it, Lds::V), rb, 16 * wave, s);
-        row_frag<T, D, true>(fk[s], tile(it, Lds::K), rb, 16 * wave, s);
+        row_frag<T>(fv[s], t0, ov, s);
+        row_frag<T>(fk[s], t0, ok, s);
       }
       const float ih = dc.hi[row], il = dc.lo[row];
       float own = 0.f;
@@ -256,12 +259,13 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
         float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
         if (J <= wave) {
           f32x4_t a = zero4(), b = zero4();
+          const uint32_t ru = at(Lds::U, 16 * J), rq = at(Lds::Q, 16 * J);
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
             Frag<T> f;
-            row_frag<T, D, true>(f, tile(it, Lds::U), rb, 16 * J, s);
+            row_frag<T>(f, t0, ru, s);
             mma(a, f, fv[s]);
-            row_frag<T, D, true>(f, tile(it, Lds::Q), rb, 16 * J, s);
+            row_frag<T>(f, t0, rq, s);
             mma(b, f, fk[s]);
           }
           const float4 jh = *(const float4*)&dc.hi[16 * J + 4 * g], jl = *(const float4*)&dc.lo[16 * J + 4 * g];

@@ -64,29 +64,27 @@ __device__ __forceinline__ uint32_t tok_base(int lane) {  // bf16: row 8 g + n /
   return sizeof(T) == 2 ? fresh<LEAN>(Tile<T, D>::quad(8 * g + (n >> 2), n & 3)) : 0;
 }
 
-// Addresses of two reads that must not be told to lie a constant apart: the compiler would make
-// one ds_read2st64_b64 of them, which takes 16 cycles where two ds_read_b64 take 5 (measured).
-template <bool LEAN>
-__device__ __forceinline__ uint32_t apart(uint32_t x) {
+// A lane's base for the rows from r0 on (a multiple of 16).  Nothing is known of how two of them
+// lie to each other: the compiler would make one ds_read2st64_b64 of two reads a constant apart,
+// which takes 16 cycles where two ds_read_b64 take 5 (measured).
+template <typename T, int D, bool LEAN>
+__device__ __forceinline__ uint32_t rows_at(uint32_t base, int r0) {
+  uint32_t x = base + r0 * Tile<T, D>::RB;
 #ifndef KDA_HOST_PASS
-  if constexpr (LEAN) asm volatile("" : "+v"(x));
-  else asm("" : "+v"(x));
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (LEAN) asm volatile("" : "+v"(x));
+    else asm("" : "+v"(x));
+  }
 #endif
   return x;
 }
 
 // row fragment of 32 columns: slots 0-3 columns 32 s + 4 g.., slots 4-7 columns 32 s + 16 + 4 g.. of
-// row r0 + n (r0 a multiple of 16): the order in which two 16-row accumulator tiles of the state
+// row r0 + n, base = rows_at(.., r0): the order in which two 16-row accumulator tiles of the state
 // hold their rows
-template <typename T, int D, bool LEAN = false>
-__device__ __forceinline__ void row_frag(Frag<T>& f, const char* t, uint32_t base, int r0, int s) {
-  uint32_t a = (base ^ (s * 32 * sizeof(T))) + r0 * Tile<T, D>::RB;
-  uint32_t b = (base ^ ((s * 32 + 16) * sizeof(T))) + r0 * Tile<T, D>::RB;
-  if constexpr (sizeof(T) == 2) {
-    a = apart<LEAN>(a);
-    b = apart<LEAN>(b);
-  }
-  f.load4x2(t + a, t + b);
+template <typename T>
+__device__ __forceinline__ void row_frag(Frag<T>& f, const char* t, uint32_t base, int s) {
+  f.load4x2(t + (base ^ (s * 32 * sizeof(T))), t + (base ^ ((s * 32 + 16) * sizeof(T))));
 }
 
 // token fragment: slots hold tokens 32 s + 8 g + e of column c0 + n (c0 a multiple of 16)
@@ -432,10 +430,10 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
   Frag<T> fq[KS], fx[DOT == kDotCross ? 2 : 1];
   const uint32_t rb = row_base<T, DK, false>(lane), vb = row_base<T, VT, false>(lane);
 #pragma unroll
-  for (int s = 0; s < KS; ++s) row_frag<T, DK>(fq[s], sQ, rb, 16 * wave, s);
+  for (int s = 0; s < KS; ++s) row_frag<T>(fq[s], sQ, rows_at<T, DK, false>(rb, 16 * wave), s);
   if constexpr (DOT == kDotCross) {
-    row_frag<T, VT>(fx[0], sX, vb, 16 * wave, 0);
-    row_frag<T, VT>(fx[1], sX, vb, 16 * wave, 1);
+    row_frag<T>(fx[0], sX, rows_at<T, VT, false>(vb, 16 * wave), 0);
+    row_frag<T>(fx[1], sX, rows_at<T, VT, false>(vb, 16 * wave), 1);
   }
   const float ih = dc.hi[row], il = dc.lo[row];
   float own_sum = 0.f;
@@ -447,14 +445,14 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         Frag<T> fk;
-        row_frag<T, DK>(fk, sK, rb, 16 * J, s);
+        row_frag<T>(fk, sK, rows_at<T, DK, false>(rb, 16 * J), s);
         mma(a, fk, fq[s]);
       }
       if constexpr (DOT == kDotCross) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           Frag<T> fv;
-          row_frag<T, VT>(fv, sV, vb, 16 * J, s);
+          row_frag<T>(fv, sV, rows_at<T, VT, false>(vb, 16 * J), s);
           mma(e, fv, fx[s]);
         }
       }
@@ -490,8 +488,12 @@ __device__ __forceinline__ void make_p(const char* sQ, const char* sK, const cha
 template <typename T, int DK, bool EXACT, bool LEAN = false>
 __device__ __forceinline__ void from_state(const f32x4_t (&S)[DK / 16], const char* sQ, int lane, f32x4_t (&acc)[4]) {
   const uint32_t rb = row_base<T, DK, LEAN>(lane);
+  uint32_t rt[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) acc[t] = zero4();
+  for (int t = 0; t < 4; ++t) {
+    rt[t] = rows_at<T, DK, LEAN>(rb, 16 * t);
+    acc[t] = zero4();
+  }
 #pragma unroll
   for (int s = 0; s < DK / 32; ++s) {
     Frag<T> fs, fm, fl;
@@ -506,7 +508,7 @@ __device__ __forceinline__ void from_state(const f32x4_t (&S)[DK / 16], const ch
     for (int t2 = 0; t2 < 4; t2 += 2) {
       Frag<T> fq[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) row_frag<T, DK, LEAN>(fq[x], sQ, rb, 16 * (t2 + x), s);
+      for (int x = 0; x < 2; ++x) row_frag<T>(fq[x], sQ, rt[t2 + x], s);
 #pragma unroll
       for (int x = 0; x < 2; ++x) mma(acc[t2 + x], fs, fq[x]);
       if constexpr (sizeof(T) == 2 && EXACT) {
