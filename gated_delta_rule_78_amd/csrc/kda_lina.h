@@ -46,6 +46,9 @@ struct LinaWalk {
 
 constexpr int kLinaGroup = 16;  // chunks between two kept states of the backward
 
+// most threads of a workgroup: walks, the decay gradient's sums, decode
+constexpr int kLinaThreads = 768, kLinaDecayThreads = 64 * kLinaGroup, kLinaDecodeThreads = 512;
+
 // Segments (or groups of `per` chunks) of a batch: sequence i starts at
 // offset / (64 per) + i, so that every sequence has at least one.
 inline int64_t lina_pieces(int64_t rows, int64_t n, int64_t per) { return rows / (64 * per) + n; }

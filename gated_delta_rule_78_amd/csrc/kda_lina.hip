@@ -34,6 +34,7 @@
 // and the state where it is multiplied by q.  In the walks that a and b are taken from, the state
 // meets its rows as three terms too: D is a small difference of long sums of a and b, and with
 // two-term operands its error was 1e-5 of the gradient's norm, now 6e-7.
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_lina_tile.h"
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
 // make the scores of the next chunk.  A step has two halves: from the states (meanwhile the next
 // tiles and this chunk's P go to LDS), then P V and the states' update (meanwhile the next scores,
 // kept in registers).  With separate walks B4 H32 T8K took 0.87 ms here.
-template <int D, bool WANT>
+template <int D>
 struct RevLds {
   static constexpr int Q = 0, K = Tile<bf16_t, D>::BYTES, V = 2 * K, U = 3 * K, TILES = 4 * K;
   static constexpr int PK = 2 * TILES, PV = PK + Tile<bf16_t, 64>::BYTES;
@@ -204,7 +205,7 @@ struct RevParams {
 template <int D, bool WANT>
 __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p) {
   typedef bf16_t T;
-  typedef RevLds<D, WANT> Lds;
+  typedef RevLds<D> Lds;
   constexpr int KS = D / 32;
   extern __shared__ __align__(16) char smem[];
   __shared__ Decays dec[2];
@@ -484,7 +485,8 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
   const LinaWalk& w = p.w;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Chain ch;
-  if (!ch.place(p, REV) || ch.tail) return;  // nobody starts from a tail's end
+  if (!ch.place(p, REV)) return;
+  if (ch.tail) return keep_start<DK>(p, ch, tid);  // nobody starts from a tail's end
   const Operand<T> k(w.k, w, ch.h, DK, 0), v(w.v, w, ch.h, w.dv, ch.vt * VT);
   Stage<T, DK> rk;
   Stage<T, VT> rv;
@@ -655,23 +657,24 @@ template <typename T>
 __global__ __launch_bounds__(256) void lina_headsum_kernel(const float* __restrict__ part, void* __restrict__ out,
                                                            int64_t quads, int heads, int group, int qd,
                                                            const int* __restrict__ end) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= quads || (end && i >= (int64_t)*end * heads * qd)) return;
-  const int64_t row = i / qd;  // (token, shared head)
-  const int c = (int)(i % qd);
-  const float4* src = (const float4*)part + (row * group) * qd + c;
-  float4 s = src[0];
-  for (int x = 1; x < group; ++x) {
-    const float4 y = src[(int64_t)x * qd];
-    s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+  if (end) quads = min(quads, (int64_t)*end * heads * qd);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / qd;  // (token, shared head)
+    const int c = (int)(i % qd);
+    const float4* src = (const float4*)part + (row * group) * qd + c;
+    float4 s = src[0];
+    for (int x = 1; x < group; ++x) {
+      const float4 y = src[(int64_t)x * qd];
+      s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    st_quad<T>((char*)out + (size_t)i * 4 * sizeof(T), v);
   }
-  const float v[4] = {s.x, s.y, s.z, s.w};
-  st_quad<T>((char*)out + (size_t)i * 4 * sizeof(T), v);
 }
 
 // dg from the walks' parts: one workgroup of 16 waves per group of 16 chunks and head,
 // wave = chunk, lane = token
-__global__ __launch_bounds__(1024) void lina_ddecay_kernel(const int* __restrict__ cs, int nseq, int T, int H,
+__global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const int* __restrict__ cs, int nseq, int T, int H,
                                                            int64_t rows, const float* __restrict__ a,
                                                            const float* __restrict__ b, const float* __restrict__ e,
                                                            int na, int ne, const float* __restrict__ anchor,
@@ -792,10 +795,10 @@ hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv) {
   }
   const bool want = wk.dot != kDotNone;
   if (wk.dk == 128)
-    return want ? launch(lina_reverse_kernel<128, true>, p, 3 * NT, RevLds<128, true>::BYTES)
-                : launch(lina_reverse_kernel<128, false>, p, 3 * NT, RevLds<128, false>::BYTES);
-  return want ? launch(lina_reverse_kernel<64, true>, p, 3 * NT, RevLds<64, true>::BYTES)
-              : launch(lina_reverse_kernel<64, false>, p, 3 * NT, RevLds<64, false>::BYTES);
+    return want ? launch(lina_reverse_kernel<128, true>, p, 3 * NT, RevLds<128>::BYTES)
+                : launch(lina_reverse_kernel<128, false>, p, 3 * NT, RevLds<128>::BYTES);
+  return want ? launch(lina_reverse_kernel<64, true>, p, 3 * NT, RevLds<64>::BYTES)
+              : launch(lina_reverse_kernel<64, false>, p, 3 * NT, RevLds<64>::BYTES);
 }
 
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream) {
@@ -808,8 +811,7 @@ hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int h
                                const int* end, void* stream) {
   const int64_t quads = rows * heads * (d / 4);
   if (quads == 0) return hipSuccess;
-  const int64_t blocks = (quads + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t blocks = std::min<int64_t>((quads + 255) / 256, 1 << 20);
   if (bf16)
     hipLaunchKernelGGL(lina_headsum_kernel<bf16_t>, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, part,
                        out, quads, heads, group, d / 4, end);
@@ -825,7 +827,7 @@ hipError_t launch_lina_ddecay(const LinaWalk& w, const float* a, const float* b,
   const int64_t per = (int64_t)C * kLinaGroup;
   const int64_t groups = w.cs ? lina_pieces(w.T, w.n, kLinaGroup) : (int64_t)w.n * (((int64_t)w.T + per - 1) / per);
   if (rows > 0 && groups > 0) {
-    hipLaunchKernelGGL(lina_ddecay_kernel, dim3((unsigned)groups, (unsigned)w.H), dim3(1024), 0,
+    hipLaunchKernelGGL(lina_ddecay_kernel, dim3((unsigned)groups, (unsigned)w.H), dim3(kLinaDecayThreads), 0,
                        (hipStream_t)w.stream, w.cs, w.n, w.T, w.H, rows, a, b, e, na, ne, anchor, w.g, w.g_fixed, dg,
                        part);
     const hipError_t er = hipGetLastError();

@@ -80,6 +80,11 @@ Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   return p;
 }
 
+// A launch counts its threads in 32 bits: no walk of this plan may have more workgroups.
+bool launchable(const Plan& p, const kda_shape& s, int qk_heads, int nv) {
+  return ((p.nseg * qk_heads + 7) / 8 * 8) * (s.H / qk_heads) * nv <= 0xFFFFFFFFll / kda::kLinaThreads;
+}
+
 struct FwdLayout {
   Plan plan;
   size_t off_dec, off_cs, off_list, bytes;
@@ -111,6 +116,7 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
     if (x && misaligned(x)) return KDA_ERR_ALIGN;
   if (misaligned(g, 4) || misaligned(cu, 4)) return KDA_ERR_ALIGN;
   const FwdLayout l = fwd_layout(s, n_seqs);
+  if (!launchable(l.plan, s, Hk, s.dv / 64)) return KDA_ERR_SHAPE;
   if (l.bytes > 0 && !ws) return KDA_ERR_NULL;
   if (ws_bytes < l.bytes) return KDA_ERR_WORKSPACE;
   if (misaligned(ws, 256)) return KDA_ERR_ALIGN;
@@ -218,6 +224,8 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
     if (x && misaligned(x)) return KDA_ERR_ALIGN;
   if (misaligned(p.g, 4) || misaligned(p.dg, 4) || misaligned(cu, 4)) return KDA_ERR_ALIGN;
   const BwdLayout l = bwd_layout(s, Hk, n_seqs);
+  if (!launchable(l.plan, s, Hk, std::max(s.dk, s.dv) / 64) || l.groups > 0xFFFFFFFFll / kda::kLinaDecayThreads)
+    return KDA_ERR_SHAPE;
   if (l.bytes > 0 && !p.ws) return KDA_ERR_NULL;
   if (p.ws_bytes < l.bytes) return KDA_ERR_WORKSPACE;
   if (misaligned(p.ws, 256)) return KDA_ERR_ALIGN;
@@ -336,6 +344,7 @@ int decode_impl(const kda_shape* shape, int Hk, int ntok, const void* q, const v
   int rc = check_lina_shape(&s, Hk, true, -1, &es);
   if (rc) return rc;
   if (ntok < 0) return KDA_ERR_SHAPE;
+  if ((int64_t)s.B * s.H * (s.dv / 64) > 0xFFFFFFFFll / kda::kLinaDecodeThreads) return KDA_ERR_SHAPE;
   const int64_t toks = (int64_t)s.B * ntok, st = (int64_t)s.B * s.H * s.dk * s.dv * 4;
   if (toks > 0 && (!q || !k || !v || !g || !state || !o)) return KDA_ERR_NULL;
   if (state && misaligned(state)) return KDA_ERR_ALIGN;

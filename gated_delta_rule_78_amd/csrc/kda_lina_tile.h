@@ -360,14 +360,25 @@ __device__ __forceinline__ void each_state(const LinaWalk& w, const Chain& ch, i
     }
 }
 
-// The state a walk starts from: the caller's, carried over the segments before this one.
+// The state a walk starts from: the caller's, carried over the segments before this one.  Of a chain
+// in several segments it comes from the last one's slot (keep_start), because that one may write
+// its final state over the caller's while others have not begun.
 template <int DK>
 __device__ __forceinline__ void start_state(const WalkParams& p, const Chain& ch, bool rev, int tid,
                                             f32x4_t (&S)[DK / 16]) {
   const LinaWalk& w = p.w;
+  const bool kept = w.split && ch.nsg > 1;
 #pragma unroll
   for (int ct = 0; ct < DK / 16; ++ct) S[ct] = zero4();
-  if (w.s0) each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
+  if (w.s0) {
+    if (kept) {
+      const f32x4_t* from = (const f32x4_t*)(w.seg_state + ch.at(p, ch.seg - ch.sg + (rev ? 0 : ch.nsg - 1)) * (DK * VT));
+#pragma unroll
+      for (int ct = 0; ct < DK / 16; ++ct) S[ct] = from[ct * NT + tid];
+    } else {
+      each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
+    }
+  }
   if (!w.split || ch.head) return;
   const int cnt = rev ? ch.nsg - 1 - ch.sg : ch.sg;
 #pragma unroll 2
@@ -382,6 +393,18 @@ __device__ __forceinline__ void start_state(const WalkParams& p, const Chain& ch
       for (int i = 0; i < 4; ++i) S[ct][i] = fmaf(S[ct][i], d, x[i]);
     }
   }
+}
+
+// The caller's start state into the slot of the chain's last segment, from whose end nobody starts.
+template <int DK>
+__device__ __forceinline__ void keep_start(const WalkParams& p, const Chain& ch, int tid) {
+  const LinaWalk& w = p.w;
+  if (!w.s0 || ch.nsg == 1) return;
+  f32x4_t* to = (f32x4_t*)(w.seg_state + ch.at(p, ch.seg) * (DK * VT));
+  f32x4_t S[DK / 16];
+  each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
+#pragma unroll
+  for (int ct = 0; ct < DK / 16; ++ct) to[ct * NT + tid] = S[ct];
 }
 
 // The caller's final state; a reverse walk's state is the gradient after the first token's decay.

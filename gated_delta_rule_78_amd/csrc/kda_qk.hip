@@ -305,6 +305,7 @@ __global__ __launch_bounds__(1024) void qk_dw_kernel(const float* __restrict__ p
 // (256 compute units, eight workgroups each), fewer where there are not.
 int heads_per_group(int64_t token_blocks, int heads) {
   int parts = 1;
+  token_blocks = token_blocks < 1 ? 1 : token_blocks;  // parts <= 2,048 = kQkMaxBlocks
   while (token_blocks * parts < 2048 && (heads + parts - 1) / parts > 1) parts *= 2;
   return (heads + parts - 1) / parts;
 }

@@ -12,7 +12,8 @@ int check_qk(const kda_qk_shape* s, int* es) {
   if (!s) return KDA_ERR_NULL;
   if (s->dtype != KDA_BF16 && s->dtype != KDA_F32) return KDA_ERR_DTYPE;
   if (s->tokens < 0 || s->q_heads < 1 || s->k_heads < 0 || s->d < 1) return KDA_ERR_SHAPE;
-  if (s->q_heads > 65535 || s->k_heads > 65535 || s->tokens > (int64_t(1) << 32)) return KDA_ERR_SHAPE;
+  if (s->q_heads > 65535 || s->k_heads > 65535 || s->tokens >= (int64_t(1) << 28))
+    return KDA_ERR_SHAPE;  // a launch counts its threads, up to 16 a token, in 32 bits
   if (!supported_width(s->d)) return KDA_ERR_UNSUPPORTED;
   if (s->norm < KDA_NORM_NONE || s->norm > KDA_NORM_L2) return KDA_ERR_UNSUPPORTED;
   if (!(s->eps >= 0.f)) return KDA_ERR_SHAPE;

@@ -446,11 +446,12 @@ int kda_gdn2_decode_tokens(const kda_shape* shape, const void* q, const void* k,
  *                    and NULL accepted, when the chains are walked whole; with fewer chains
  *                    than compute units it holds the end states of their segments)
  * Arithmetic: fp32 sums, decays and states; with bf16 inputs the products r o q.k and the state
- * as q meets it are rounded to bf16 (as o is); what is added to the state is kept to 2^-16.
+ * as q meets it are rounded to bf16 (as o is); what is added to the state is kept to 2^-24.
  * A non-finite v_t reaches the outputs from token t on only.  Alignment: 16 bytes for q, k, v,
  * o and the states, 4 for log_decay.  Aliasing, packed batches (cu_seqlens, n_seqs, states of
  * [n_seqs, H, dk, dv], token rows after the last offset not written) and errors as
- * kda_chunk_fwd_ws and kda_chunk_fwd_varlen.  H <= 65535.
+ * kda_chunk_fwd_ws and kda_chunk_fwd_varlen.  H <= 65535; n_seqs <= 2^24; more than about
+ * 5.5 million (sequence segment, head, 64 value columns) are KDA_ERR_SHAPE.
  */
 size_t kda_lina_chunk_fwd_workspace_size(const kda_shape* shape); /* 0 also if the shape is invalid */
 int kda_lina_chunk_fwd(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
@@ -528,7 +529,7 @@ int kda_lina_decode_tokens(const kda_shape* shape, int qk_heads, const void* q, 
 typedef enum { KDA_NORM_NONE = 0, KDA_NORM_RMS = 1, KDA_NORM_L2 = 2 } kda_norm;
 
 typedef struct {
-    long long tokens;   /* B * T, >= 0 */
+    long long tokens;   /* B * T, 0 <= tokens < 2^28 */
     int q_heads, k_heads;
     int d;
     long long q_stride, k_stride;

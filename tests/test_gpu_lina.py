@@ -107,6 +107,23 @@ def test_forward_in_segments(B, T, Hk, H, dtype):
     _check_fwd(B, T, Hk, H, 128 if H < 8 else 64, 64, dtype, seed=T)
 
 
+@pytest.mark.parametrize("B,T,Hk,H,packed", [(1, 1500, 1, 3, False), (2, 4096, 32, 64, False), (1, 5000, 4, 8, True)])
+def test_state_in_place_over_segments(B, T, Hk, H, packed):
+    """final_state may be initial_state: a segment that ends early must not be read as the start."""
+    import torch
+    import gated_delta_rule_78_amd as kda
+    q, k, v, g = _dev(*_inputs(B, T, Hk, H, 64, 128, "bf16")[:4])
+    cu, s0 = None, torch.randn(B, H, 64, 128, device="cuda")
+    if packed:
+        cu = torch.tensor([0, 0, 64 * 60 + 1, 64 * 60 + 20, T], dtype=torch.int32, device="cuda")
+        s0 = torch.randn(4, H, 64, 128, device="cuda")
+    o, st = kda.lina_chunk_fwd(q, k, v, g, initial_state=s0, cu_seqlens=cu)
+    for _ in range(3):
+        s = s0.clone()
+        o2, st2 = kda.lina_chunk_fwd(q, k, v, g, initial_state=s, final_state=s, cu_seqlens=cu)
+        assert st2 is s and torch.equal(o, o2) and torch.equal(st, s)
+
+
 def _decays(kind, B, T, H):
     import torch
     r = torch.Generator().manual_seed(5)

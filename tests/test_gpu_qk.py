@@ -128,6 +128,17 @@ def test_weight_gradient_of_many_rows():
     assert float(((a[2].double() - want).abs() / (z * hat).abs().sum((0, 1, 2))).max()) <= 2.0 ** -20
 
 
+def test_weight_gradients_without_a_token():
+    """No rows: zeros, also with more heads than the parts that the weight gradients are summed from."""
+    import torch
+
+    import gated_delta_rule_78_amd as kda
+    for H in (2, 5000):
+        q, w = torch.empty(1, 0, H, 64, device="cuda"), torch.ones(64, device="cuda")
+        _, _, gw, _ = kda.qk_norm_rope_bwd(q, None, q, q_weight=w)
+        assert torch.equal(gw, torch.zeros_like(w))
+
+
 def test_in_place_and_single_tokens():
     import torch
 

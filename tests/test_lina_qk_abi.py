@@ -80,6 +80,15 @@ def test_lina_refuses_sizes(L):
     assert _fwd(L, chunk=32) == UNSUP and _bwd(L, chunk=32) == UNSUP
 
 
+def test_lina_refuses_more_than_a_launch_holds(L):
+    """A launch counts its threads in 32 bits: more workgroups than that are refused before the first."""
+    n = 1 << 23
+    assert _fwd(L, T=64, varlen=n, cu=_p(13)) == SHAPE and _bwd(L, T=64, varlen=n, cu=_p(13)) == SHAPE
+    assert _fwd(L, B=1 << 23, T=1, H=1, Hk=1) == SHAPE and _bwd(L, B=1 << 23, T=1, H=1, Hk=1) == SHAPE
+    assert _bwd(L, B=5 << 20, T=1, H=1, Hk=1) == SHAPE
+    assert _dec(L, B=1 << 20, H=8, Hk=8, dv=128) == SHAPE
+
+
 def test_lina_refuses_alignment(L):
     for name in ("q", "k", "v", "o"):
         assert _fwd(L, **{name: _p(5, 8)}) == ALIGN
@@ -158,6 +167,7 @@ def test_qk_refusals(L, bwd):
     assert f(rot=128) == SHAPE and f(rot=-16) == SHAPE and f(rot=24, sec=(12, 0, 0, 0)) == UNSUP
     assert f(axes=0) == UNSUP and f(axes=5) == UNSUP
     assert f(axes=3, sec=(8, 12, 8, 0)) == SHAPE and f(axes=2, sec=(-8, 40, 0, 0)) == SHAPE
+    assert f(tokens=1 << 28) == SHAPE
     assert f(qs=127) == SHAPE and f(ks=63) == SHAPE and f(qs=132) == ALIGN
     for nm in ("q", "k", "inv", "pos", "oq", "ok") + (("dyq", "dyk") if bwd else ()):
         assert f(**{nm: NUL}) == NULL, nm
