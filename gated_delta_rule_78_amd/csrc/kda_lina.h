@@ -53,7 +53,11 @@ constexpr int kLinaThreads = 768, kLinaDecayThreads = 64 * kLinaGroup, kLinaDeco
 // offset / (64 per) + i, so that every sequence has at least one.
 inline int64_t lina_pieces(int64_t rows, int64_t n, int64_t per) { return rows / (64 * per) + n; }
 
+// up to three walks of one call: the end states of their segments, where they are split
+hipError_t launch_lina_segments(const LinaWalk* w, int n);
 hipError_t launch_lina_walk(const LinaWalk& w);
+// dq's and dv's walk in one launch: fp32
+hipError_t launch_lina_pair(const LinaWalk& wq, const LinaWalk& wv);
 // dk's and dv's walk in one kernel: bf16, widths equal; wv.x: v
 hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv);
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream);

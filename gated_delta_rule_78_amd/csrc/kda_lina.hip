@@ -71,7 +71,7 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
   const LinaWalk& w = p.w;
   const int tid = threadIdx.x & (NT - 1), lane = tid & 63, wave = tid >> 6;
   Chain ch;
-  if (!ch.place(p, REV)) return;
+  if (!ch.place(p, REV, blockIdx.x)) return;
   const int steps = ch.last - ch.first;
   auto chunk = [&](int it) { return REV ? ch.last - 1 - it : ch.first + it; };
   const Operand<T> x(w.x, w, ch.h, w.dv, ch.vt * VT);
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
 
   const int tid = threadIdx.x & (NT - 1), lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
   Chain ch;
-  if (!ch.place(p.k, true)) return;
+  if (!ch.place(p.k, true, blockIdx.x)) return;
   const int steps = ch.last - ch.first;
   auto chunk = [&](int it) { return ch.last - 1 - it; };
   const int role = threadIdx.x / NT;
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
 
 // fp32: one workgroup of four waves, one tile buffer, chunk after chunk.
 template <int DK, bool REV, int DOT>
-__global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
+__device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned block) {
   typedef float T;
   typedef Tile<T, DK> KT;
   typedef Tile<T, VT> VTl;
@@ -409,7 +409,7 @@ __global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
   const LinaWalk& w = p.w;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Chain ch;
-  if (!ch.place(p, REV)) return;
+  if (!ch.place(p, REV, block)) return;
   const Operand<T> q(w.q, w, ch.h, DK, 0), k(w.k, w, ch.h, DK, 0), v(w.v, w, ch.h, w.dv, ch.vt * VT),
       x(w.x, w, ch.h, w.dv, ch.vt * VT);
   Stage<T, DK> rq, rk;
@@ -475,32 +475,60 @@ __global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
   store_state<DK, REV>(p, ch, tid, S);
 }
 
+template <int DK, bool REV, int DOT>
+__global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
+  walk_f32_body<DK, REV, DOT>(p, blockIdx.x);
+}
+
+// The walks of dq and dv side by side: they need nothing of each other, and fp32 calls are seldom
+// large enough to fill the machine with one.
+struct PairParams {
+  WalkParams q, v;
+  unsigned blocks_q;
+};
+
+template <int DKQ, int DKV, bool WANT>
+__global__ __launch_bounds__(NT) void lina_pair_f32_kernel(const PairParams p) {
+  if (blockIdx.x < p.blocks_q) walk_f32_body<DKQ, false, WANT ? kDotRow : kDotNone>(p.q, blockIdx.x);
+  else walk_f32_body<DKV, true, WANT ? kDotCross : kDotNone>(p.v, blockIdx.x - p.blocks_q);
+}
+
 // End states of the segments from a zero start: the walk without its outputs.  Two tile
-// buffers, one barrier per chunk; small enough for three workgroups on a compute unit.
-template <typename T, int DK, bool REV>
-__global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
+// buffers, one barrier per chunk; small enough for three workgroups on a compute unit.  Walks of one
+// call that have d_k in common (the backward's three) go in one launch.
+struct SegParams {
+  WalkParams p[3];
+  unsigned end[3];  // their workgroups, running sums
+};
+
+template <typename T, int DK>
+__global__ __launch_bounds__(NT) void lina_segment_kernel(const SegParams all) {
+  const int which = (blockIdx.x >= all.end[0]) + (blockIdx.x >= all.end[1]);
+  const WalkParams& p = all.p[which];
+  const unsigned block = blockIdx.x - (which ? all.end[which - 1] : 0);
+  const bool rev = p.w.rev;
   constexpr int TILES = Tile<T, DK>::BYTES + Tile<T, VT>::BYTES;
   extern __shared__ __align__(16) char smem[];
   __shared__ Decays dec[2];
   const LinaWalk& w = p.w;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Chain ch;
-  if (!ch.place(p, REV)) return;
+  if (!ch.place(p, rev, block)) return;
   if (ch.tail) return keep_start<DK>(p, ch, tid);  // nobody starts from a tail's end
   const Operand<T> k(w.k, w, ch.h, DK, 0), v(w.v, w, ch.h, w.dv, ch.vt * VT);
   Stage<T, DK> rk;
   Stage<T, VT> rv;
   float rg = 0.f;
   const int steps = ch.last - ch.first;
-  auto chunk = [&](int it) { return REV ? ch.last - 1 - it : ch.first + it; };
+  auto chunk = [&](int it) { return rev ? ch.last - 1 - it : ch.first + it; };
   auto fetch = [&](int it) {
     if (it >= steps) return;
     const int c = chunk(it);
     const int64_t t = ch.lo + (int64_t)c * C;
     const uint32_t n = ch.rows(c);
-    if (wave == 0) rg = row_decay<REV>(w, ch, c, lane);
-    rk.load(k.rows(t, n), k.step, REV, tid);
-    rv.load(v.rows(t, n), v.step, REV, tid);
+    if (wave == 0) rg = rev ? row_decay<true>(w, ch, c, lane) : row_decay<false>(w, ch, c, lane);
+    rk.load(k.rows(t, n), k.step, rev, tid);
+    rv.load(v.rows(t, n), v.step, rev, tid);
   };
   auto put = [&](int it) {
     if (it >= steps) return;
@@ -535,25 +563,20 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const WalkParams p) {
   if (tid == 0 && ch.vt == 0) w.seg_dec[(size_t)ch.seg * w.H + ch.h] = total;
 }
 
-inline const WalkParams& chain_of(const WalkParams& p) { return p; }
-inline const WalkParams& chain_of(const RevParams& p) { return p.k; }
-
 template <typename K, typename P>
-hipError_t launch(K kern, const P& p, int threads, int lds) {
-  const WalkParams& c = chain_of(p);
-  const unsigned blocks = walk_blocks(c);
-  if (blocks == 0) return hipErrorInvalidValue;
+hipError_t launch(K kern, const P& p, unsigned blocks, int threads, int lds, void* stream) {
+  if (blocks == 0) return hipSuccess;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kern, dim3(blocks), dim3(threads), lds, (hipStream_t)c.w.stream, p);
+  hipLaunchKernelGGL(kern, dim3(blocks), dim3(threads), lds, (hipStream_t)stream, p);
   return hipGetLastError();
 }
 
 template <int DK, bool REV, int DOT>
 hipError_t walk_bf16(const WalkParams& p) {
-  return launch(lina_walk_bf16_kernel<DK, REV, DOT>, p, 2 * NT, PipeLds<DK, DOT>::BYTES);
+  return launch(lina_walk_bf16_kernel<DK, REV, DOT>, p, walk_blocks(p), 2 * NT, PipeLds<DK, DOT>::BYTES, p.w.stream);
 }
 
 template <int DK>
@@ -564,25 +587,48 @@ hipError_t walk_bf16(const WalkParams& p) {
   return w.rev ? walk_bf16<DK, true, kDotNone>(p) : walk_bf16<DK, false, kDotNone>(p);
 }
 
+template <int DK, int DOT>
+constexpr int kF32Lds = 2 * Tile<float, DK>::BYTES + (DOT == kDotCross ? 3 : 2) * Tile<float, 64>::BYTES;
+
 template <int DK, bool REV, int DOT>
 hipError_t walk_f32(const WalkParams& p) {
-  return launch(lina_walk_f32_kernel<DK, REV, DOT>, p, NT,
-                2 * Tile<float, DK>::BYTES + (DOT == kDotCross ? 3 : 2) * Tile<float, 64>::BYTES);
+  return launch(lina_walk_f32_kernel<DK, REV, DOT>, p, walk_blocks(p), NT, kF32Lds<DK, DOT>, p.w.stream);
 }
 
 template <int DK>
-hipError_t walk_f32(const WalkParams& p) {
+hipError_t walk_f32(const WalkParams& p) {  // the others go in pairs
   const LinaWalk& w = p.w;
-  if (w.dot == kDotCross) return w.rev ? walk_f32<DK, true, kDotCross>(p) : hipErrorInvalidValue;
-  if (w.dot == kDotRow) return w.rev ? walk_f32<DK, true, kDotRow>(p) : walk_f32<DK, false, kDotRow>(p);
-  return w.rev ? walk_f32<DK, true, kDotNone>(p) : walk_f32<DK, false, kDotNone>(p);
+  if (!w.rev) return w.dot == kDotNone ? walk_f32<DK, false, kDotNone>(p) : hipErrorInvalidValue;
+  if (w.dot == kDotCross) return hipErrorInvalidValue;
+  return w.dot == kDotRow ? walk_f32<DK, true, kDotRow>(p) : walk_f32<DK, true, kDotNone>(p);
+}
+
+template <int DKQ, int DKV, bool WANT>
+hipError_t pair_f32(const PairParams& p) {
+  constexpr int a = kF32Lds<DKQ, kDotNone>, b = kF32Lds<DKV, WANT ? kDotCross : kDotNone>;
+  return launch(lina_pair_f32_kernel<DKQ, DKV, WANT>, p, p.blocks_q + walk_blocks(p.v), NT, a > b ? a : b,
+                p.q.w.stream);
+}
+
+template <int DKQ, int DKV>
+hipError_t pair_f32(const PairParams& p) {
+  return p.q.w.dot == kDotNone ? pair_f32<DKQ, DKV, false>(p) : pair_f32<DKQ, DKV, true>(p);
 }
 
 template <typename T, int DK>
-hipError_t segments(const WalkParams& p) {
-  const int lds = 2 * (Tile<T, DK>::BYTES + Tile<T, VT>::BYTES);
-  return p.w.rev ? launch(lina_segment_kernel<T, DK, true>, p, NT, lds)
-                 : launch(lina_segment_kernel<T, DK, false>, p, NT, lds);
+hipError_t segments(const SegParams& p) {
+  return launch(lina_segment_kernel<T, DK>, p, p.end[2], NT, 2 * (Tile<T, DK>::BYTES + Tile<T, VT>::BYTES),
+                p.p[0].w.stream);
+}
+
+WalkParams walk_params(const LinaWalk& w) {
+  WalkParams p;
+  p.w = w;
+  p.nv = w.dv / VT;
+  p.rows = w.cs ? w.T : (int64_t)w.n * w.T;
+  const int64_t nch = ((int64_t)w.T + C - 1) / C;
+  p.nseg = w.cs ? lina_pieces(w.T, w.n, w.L) : (int64_t)w.n * (nch > 0 ? (nch + w.L - 1) / w.L : 1);
+  return p;
 }
 
 // Packed offsets clamped to [0, T] and made non-decreasing (a running maximum), cs[0] = 0, and
@@ -759,46 +805,58 @@ __global__ __launch_bounds__(256) void lina_ddecay_sum_kernel(const double* __re
 
 }  // namespace
 
-hipError_t launch_lina_walk(const LinaWalk& w) {
-  WalkParams p;
-  p.w = w;
-  p.nv = w.dv / VT;
-  p.rows = w.cs ? w.T : (int64_t)w.n * w.T;
-  const int64_t nch = ((int64_t)w.T + C - 1) / C;
-  p.nseg = w.cs ? lina_pieces(w.T, w.n, w.L) : (int64_t)w.n * (nch > 0 ? (nch + w.L - 1) / w.L : 1);
-  if (p.nseg == 0) return hipSuccess;
-  if (w.split) {
-    const hipError_t e = w.bf16 ? (w.dk == 128 ? segments<bf16_t, 128>(p) : segments<bf16_t, 64>(p))
-                                : (w.dk == 128 ? segments<float, 128>(p) : segments<float, 64>(p));
+hipError_t launch_lina_segments(const LinaWalk* w, int n) {
+  bool done[3] = {false, false, false};
+  for (int i = 0; i < n; ++i) {
+    if (done[i] || !w[i].split) continue;
+    SegParams p;
+    int m = 0;
+    unsigned end = 0;
+    for (int j = i; j < n; ++j)
+      if (w[j].dk == w[i].dk) {
+        p.p[m] = walk_params(w[j]);
+        p.end[m] = end += walk_blocks(p.p[m]);
+        ++m;
+        done[j] = true;
+      }
+    for (; m < 3; ++m) {
+      p.p[m] = p.p[0];
+      p.end[m] = end;
+    }
+    const hipError_t e = w[i].bf16 ? (w[i].dk == 128 ? segments<bf16_t, 128>(p) : segments<bf16_t, 64>(p))
+                                   : (w[i].dk == 128 ? segments<float, 128>(p) : segments<float, 64>(p));
     if (e != hipSuccess) return e;
   }
+  return hipSuccess;
+}
+
+hipError_t launch_lina_walk(const LinaWalk& w) {
+  const WalkParams p = walk_params(w);
   if (w.bf16) return w.dk == 128 ? walk_bf16<128>(p) : walk_bf16<64>(p);
   return w.dk == 128 ? walk_f32<128>(p) : walk_f32<64>(p);
 }
 
+hipError_t launch_lina_pair(const LinaWalk& wq, const LinaWalk& wv) {
+  PairParams p;
+  p.q = walk_params(wq);
+  p.v = walk_params(wv);
+  p.blocks_q = walk_blocks(p.q);
+  if (wq.dk == 128) return wv.dk == 128 ? pair_f32<128, 128>(p) : pair_f32<128, 64>(p);
+  return wv.dk == 128 ? pair_f32<64, 128>(p) : pair_f32<64, 64>(p);
+}
+
+template <int D, bool WANT>
+static hipError_t reverse(const RevParams& p) {
+  return launch(lina_reverse_kernel<D, WANT>, p, walk_blocks(p.k), 3 * NT, RevLds<D>::BYTES, p.k.w.stream);
+}
+
 hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv) {
   RevParams p;
-  p.k.w = wk;
-  p.v.w = wv;
-  for (WalkParams* x : {&p.k, &p.v}) {
-    LinaWalk& w = x->w;
-    w.rev = true;
-    x->nv = w.dv / VT;
-    x->rows = w.cs ? w.T : (int64_t)w.n * w.T;
-    const int64_t nch = ((int64_t)w.T + C - 1) / C;
-    x->nseg = w.cs ? lina_pieces(w.T, w.n, w.L) : (int64_t)w.n * (nch > 0 ? (nch + w.L - 1) / w.L : 1);
-    if (x->nseg == 0) return hipSuccess;
-    if (w.split) {
-      const hipError_t e = w.dk == 128 ? segments<bf16_t, 128>(*x) : segments<bf16_t, 64>(*x);
-      if (e != hipSuccess) return e;
-    }
-  }
+  p.k = walk_params(wk);
+  p.v = walk_params(wv);
   const bool want = wk.dot != kDotNone;
-  if (wk.dk == 128)
-    return want ? launch(lina_reverse_kernel<128, true>, p, 3 * NT, RevLds<128>::BYTES)
-                : launch(lina_reverse_kernel<128, false>, p, 3 * NT, RevLds<128>::BYTES);
-  return want ? launch(lina_reverse_kernel<64, true>, p, 3 * NT, RevLds<64>::BYTES)
-              : launch(lina_reverse_kernel<64, false>, p, 3 * NT, RevLds<64>::BYTES);
+  if (wk.dk == 128) return want ? reverse<128, true>(p) : reverse<128, false>(p);
+  return want ? reverse<64, true>(p) : reverse<64, false>(p);
 }
 
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream) {

@@ -162,15 +162,16 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
         hipSuccess)
       return KDA_ERR_HIP;
   }
+  if (kda::launch_lina_segments(&a, 1) != hipSuccess) return KDA_ERR_HIP;
   return kda::launch_lina_walk(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
-// Workspace of the backward: segment states (the three walks use them in turn), kept states
+// Workspace of the backward: segment states of the three walks, kept states
 // and per-token parts of the decay gradient, the per-head gradients of shared q and k.
 struct BwdLayout {
   Plan plan;
   int64_t groups;
-  size_t off_dec, off_seg2, off_dec2, off_cs, off_list, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
+  size_t off_dec, off_seg2, off_dec2, off_seg3, off_dec3, off_cs, off_list, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
 };
 
 BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
@@ -183,7 +184,9 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   l.off_dec = up(seg * state);
   l.off_seg2 = up(l.off_dec + seg * s.H * 4);
   l.off_dec2 = up(l.off_seg2 + seg * state);
-  l.off_cs = up(l.off_dec2 + seg * s.H * 4);
+  l.off_seg3 = up(l.off_dec2 + seg * s.H * 4);
+  l.off_dec3 = up(l.off_seg3 + seg * state);
+  l.off_cs = up(l.off_dec3 + seg * s.H * 4);
   l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
   l.off_snap = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
   l.off_anchor = up(l.off_snap + l.groups * state);
@@ -276,60 +279,62 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
   float* anchor = (float*)(ws + l.off_anchor);
   float *da = (float*)(ws + l.off_a), *db = (float*)(ws + l.off_b), *de = (float*)(ws + l.off_e);
   const kda::LinaOp q{p.q, Hk}, k{p.k, Hk}, v{p.v, s.H}, u{p.d_o, s.H};
-  kda::LinaWalk wk;
-  if (toks > 0) {
-    kda::LinaWalk w = a;  // dq
-    w.q = u;
-    w.k = v;
-    w.v = k;
-    w.x = q;
-    w.dk = s.dv;
-    w.dv = s.dk;
-    w.out = shared ? (void*)share : p.dq;
-    w.out_f32 = shared;
-    w.s0 = p.s0;
-    w.s_t = true;
-    w.dot = p.dg ? kda::kDotRow : kda::kDotNone;
-    w.dots = da;
-    w.snap = (float*)(ws + l.off_snap);
-    if (kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
-    if (shared && kda::launch_lina_headsum(share, p.dq, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) != hipSuccess)
-      return KDA_ERR_HIP;
-    wk = w;  // dk
-    wk.q = v;
-    wk.k = u;
-    wk.v = q;
-    wk.x = k;
-    wk.out = shared ? (void*)share : p.dk;
-    wk.s0 = p.dsT;
-    wk.rev = true;
-    wk.dots = db;
-    wk.anchor = anchor;
-  }
-  kda::LinaWalk w = a;  // dv and the start state's gradient
-  w.q = k;
-  w.k = q;
-  w.v = u;
-  w.x = v;
-  w.dk = s.dk;
-  w.dv = s.dv;
-  w.out = p.dv;
-  w.s0 = p.dsT;
-  w.sT = p.ds0;
-  w.rev = true;
-  w.dot = p.dg ? kda::kDotCross : kda::kDotNone;
-  w.dots = de;
-  w.seg_state = (float*)(ws + l.off_seg2);
-  w.seg_dec = (float*)(ws + l.off_dec2);
+  kda::LinaWalk walks[3] = {a, a, a};
+  kda::LinaWalk &wq = walks[0], &wk = walks[1], &wv = walks[2];
+  wq.q = u;
+  wq.k = v;
+  wq.v = k;
+  wq.x = q;
+  wq.dk = s.dv;
+  wq.dv = s.dk;
+  wq.out = shared ? (void*)share : p.dq;
+  wq.out_f32 = shared;
+  wq.s0 = p.s0;
+  wq.s_t = true;
+  wq.dot = p.dg ? kda::kDotRow : kda::kDotNone;
+  wq.dots = da;
+  wq.snap = (float*)(ws + l.off_snap);
+  wk = wq;
+  wk.q = v;
+  wk.k = u;
+  wk.v = q;
+  wk.x = k;
+  wk.out = shared ? (void*)share : p.dk;
+  wk.s0 = p.dsT;
+  wk.rev = true;
+  wk.dots = db;
+  wk.anchor = anchor;
+  wk.seg_state = (float*)(ws + l.off_seg2);
+  wk.seg_dec = (float*)(ws + l.off_dec2);
+  wv.q = k;  // and the start state's gradient
+  wv.k = q;
+  wv.v = u;
+  wv.x = v;
+  wv.dk = s.dk;
+  wv.dv = s.dv;
+  wv.out = p.dv;
+  wv.s0 = p.dsT;
+  wv.sT = p.ds0;
+  wv.rev = true;
+  wv.dot = p.dg && toks > 0 ? kda::kDotCross : kda::kDotNone;
+  wv.dots = de;
+  wv.seg_state = (float*)(ws + l.off_seg3);
+  wv.seg_dec = (float*)(ws + l.off_dec3);
+  if (toks == 0) return kda::launch_lina_walk(wv) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+  if (kda::launch_lina_segments(walks, 3) != hipSuccess) return KDA_ERR_HIP;
+  auto sum_heads = [&](void* to) {
+    return shared ? kda::launch_lina_headsum(share, to, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) : hipSuccess;
+  };
+  // dk after dq, whose kept states it meets; dv with one of them
   const bool fused = a.bf16 && s.dk == s.dv;
-  if (toks > 0) {
-    if ((fused ? kda::launch_lina_reverse(wk, w) : kda::launch_lina_walk(wk)) != hipSuccess) return KDA_ERR_HIP;
-    if (shared && kda::launch_lina_headsum(share, p.dk, toks, Hk, s.H / Hk, s.dk, a.bf16, end, stream) != hipSuccess)
-      return KDA_ERR_HIP;
-  }
-  if (!(toks > 0 && fused) && kda::launch_lina_walk(w) != hipSuccess) return KDA_ERR_HIP;
-  if (p.dg && toks > 0 &&
-      kda::launch_lina_ddecay(w, da, db, de, s.dk / 64, s.dv / 64, anchor, p.per_head ? nullptr : p.dg,
+  if ((a.bf16 ? kda::launch_lina_walk(wq) : kda::launch_lina_pair(wq, wv)) != hipSuccess || sum_heads(p.dq) != hipSuccess)
+    return KDA_ERR_HIP;
+  if ((fused ? kda::launch_lina_reverse(wk, wv) : kda::launch_lina_walk(wk)) != hipSuccess ||
+      sum_heads(p.dk) != hipSuccess)
+    return KDA_ERR_HIP;
+  if (a.bf16 && !fused && kda::launch_lina_walk(wv) != hipSuccess) return KDA_ERR_HIP;
+  if (p.dg &&
+      kda::launch_lina_ddecay(wv, da, db, de, s.dk / 64, s.dv / 64, anchor, p.per_head ? nullptr : p.dg,
                               (double*)(ws + l.off_part), p.per_head ? p.dg : nullptr) != hipSuccess)
     return KDA_ERR_HIP;
   return KDA_OK;

@@ -277,13 +277,13 @@ struct Chain {
 
   // Heads that share q and k, and the value tiles of a head, go to one XCD (workgroups are
   // dealt to the eight in turn), next to each other.  False: nothing to do here.
-  __device__ __forceinline__ bool place(const WalkParams& p, bool rev) {
+  __device__ __forceinline__ bool place(const WalkParams& p, bool rev, unsigned block) {
     const LinaWalk& w = p.w;
     const int qk = w.q.heads < w.k.heads ? w.q.heads : w.k.heads;
     const int hk = qk < w.v.heads ? qk : w.v.heads;
     const int share = w.H / hk * p.nv;
-    const int64_t slot = blockIdx.x >> 3;
-    const int64_t unit = slot / share * 8 + (blockIdx.x & 7);
+    const int64_t slot = block >> 3;
+    const int64_t unit = slot / share * 8 + (block & 7);
     const int in = (int)(slot % share);
     seg = unit / hk;
     if (seg >= p.nseg) return false;
