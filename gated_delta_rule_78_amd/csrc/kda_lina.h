@@ -40,6 +40,7 @@ struct LinaWalk {
   int H = 0, dk = 0, dv = 0;  // the walk's own widths: Q, K have dk channels, V, out dv
   int L = 0;                  // chunks of a segment
   bool split = false;         // segments are walked apart (L < the longest chain)
+  bool replay = false;        // forward: a segment's state from all chunks before it, by itself
   bool bf16 = true;
   void* stream = nullptr;
 };

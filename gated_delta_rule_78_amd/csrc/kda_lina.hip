@@ -124,14 +124,14 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
     if (steps > 1) put_from(rb, 1);
     fetch_decay(gb, 3);
     if (steps > 3) fetch_to(rb, 3);
-    scores(0);
+    if (ch.skip == 0) scores(0);
     lds_barrier();
     auto step = [&](Tiles& r, float& g, int it) {
       if (it + 2 < steps) put_from(r, it + 2);
       decays(g, it + 2);
       fetch_decay(g, it + 4);
       if (it + 4 < steps) fetch_to(r, it + 4);
-      if (it + 1 < steps) scores(it + 1);
+      if (it + 1 < steps && it + 1 >= ch.skip) scores(it + 1);
       if constexpr (DOT == kDotRow)
         if (wave == 0 && it > 0) store_dots<DOT, REV>(p, ch, chunk(it - 1), sdot[(it - 1) & 1], sdot2[0], lane);
       lds_barrier();
@@ -155,7 +155,17 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       lds_barrier();
       lds_barrier();
     }
-    for (int it = 0; it < steps; ++it) {
+    auto values = [&](Frag<T> (&fv)[2], int it) {
+      tok_frag<T, VT>(fv[0], tV(it), tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
+      tok_frag<T, VT>(fv[1], tV(it), tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
+    };
+    for (int it = 0; it < ch.skip; ++it) {
+      Frag<T> fv[2];
+      values(fv, it);
+      add_chunk<T, DK>(S, fv, tK(it), dec[it % 3], lane);
+      lds_barrier();
+    }
+    for (int it = ch.skip; it < steps; ++it) {
       const int c = chunk(it);
       const Decays& dc = dec[it % 3];
       if constexpr (DOT == kDotRow) {
@@ -170,8 +180,7 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       if constexpr (DOT == kDotCross)
         if (wave == 0) store_dots<DOT, REV>(p, ch, c, sdot[it & 1], sdot2[it & 1], lane);
       Frag<T> fv[2];
-      tok_frag<T, VT>(fv[0], tV(it), tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
-      tok_frag<T, VT>(fv[1], tV(it), tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
+      values(fv, it);
       add_intra<T, VT>(acc, fv, tP(it), tV(it), 16 * wave, lane);
       store_out<T, REV>(acc, w, ch, c, wave, lane);
       add_chunk<T, DK>(S, fv, tK(it), dc, lane);
@@ -453,6 +462,16 @@ __device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned bloc
     if (it + 2 < steps) fetch_decay(chunk(it + 2));
     if (it + 1 < steps) fetch(chunk(it + 1));
     lds_barrier();
+    Frag<T> fv[2];
+    auto values = [&] {
+      tok_frag<T, VT>(fv[0], sV, tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
+      tok_frag<T, VT>(fv[1], sV, tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
+    };
+    if (it < ch.skip) {
+      values();
+      add_chunk<T, DK>(S, fv, sK, dc, lane);
+      continue;
+    }
     if constexpr (DOT == kDotRow && !REV)
       if (c % kLinaGroup == 0) store_snap<DK>(p, ch, c, tid, S);
     make_p<T, DK, DOT>(sQ, sK, sV, sX, sP, dc, sdot[wave], sdot2, wave, lane);
@@ -463,9 +482,7 @@ __device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned bloc
     lds_barrier();
     if constexpr (DOT != kDotNone)
       if (wave == 1) store_dots<DOT, REV>(p, ch, c, sdot, sdot2, lane);
-    Frag<T> fv[2];
-    tok_frag<T, VT>(fv[0], sV, tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
-    tok_frag<T, VT>(fv[1], sV, tok_base<T, VT, false>(lane), 16 * wave, 1, lane);
+    values();
     add_intra<T, VT>(acc, fv, sP, sV, 16 * wave, lane);
     store_out<T, REV>(acc, w, ch, c, wave, lane);
     add_chunk<T, DK>(S, fv, sK, dc, lane);

@@ -33,6 +33,7 @@ int check_lina_shape(const kda_shape* s, int qk_heads, bool decode, int n_seqs, 
 struct Plan {
   int L;  // chunks of a segment
   bool split;
+  bool replay;  // the forward's segments make their start states themselves
   int64_t nseg;
 };
 
@@ -58,6 +59,10 @@ int segment_override() {
 // are dealt longest first; 256 or more are cut only where one alone would take twice as long as
 // all of them spread evenly (6 prompts of 20,011 tokens, H = 32: 241 us whole, 331 at L = 80; 24:
 // 217 and 262).
+// Of the shortest chains every segment makes its start state itself, from the chunks before it,
+// which saves the first pass and its launch: bf16, 8 heads, d = 128: 3 chunks 10.3 us against
+// 12.9, 8 chunks 16.8 and 17.4, 10 chunks 19.1 and 17.6; fp32, whose steps are dearer, 4 heads,
+// d = 64: 3 chunks 16.0 and 17.2, 4 chunks 18.8 and 17.7.
 Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   const bool packed = n_seqs >= 0;
   const int64_t nch = std::max<int64_t>(1, ((int64_t)s.T + 63) / 64);
@@ -76,6 +81,7 @@ Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   Plan p;
   p.L = (int)L;
   p.split = L < nch;
+  p.replay = p.split && nch <= (s.dtype == KDA_BF16 ? 8 : 3);
   p.nseg = packed ? kda::lina_pieces(s.T, n, L) : n * ((nch + L - 1) / L);
   return p;
 }
@@ -93,7 +99,7 @@ struct FwdLayout {
 FwdLayout fwd_layout(const kda_shape& s, int n_seqs) {
   FwdLayout l;
   l.plan = lina_plan(s, n_seqs, s.dv / 64);
-  const size_t seg = l.plan.split ? (size_t)l.plan.nseg : 0;
+  const size_t seg = l.plan.split && !l.plan.replay ? (size_t)l.plan.nseg : 0;
   l.off_dec = up(seg * s.H * s.dk * s.dv * 4);
   l.off_cs = up(l.off_dec + seg * s.H * 4);
   l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
@@ -150,7 +156,12 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
   a.dk = s.dk;
   a.dv = s.dv;
   a.L = l.plan.L;
-  a.split = l.plan.split;
+  a.split = l.plan.split && !l.plan.replay;
+  a.replay = l.plan.replay;
+  if (a.replay && s0 && s0 == sT) {  // others would read what the last segment writes: chains whole
+    a.L = (s.T + 63) / 64;
+    a.replay = false;
+  }
   a.seg_state = (float*)w;
   a.seg_dec = (float*)(w + l.off_dec);
   a.bf16 = s.dtype == KDA_BF16;

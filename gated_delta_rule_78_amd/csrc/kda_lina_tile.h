@@ -272,7 +272,8 @@ struct Chain {
   int h, vt, sq;        // head, value tile, sequence
   int sg, nsg;          // segment of the sequence, its segments
   int nch;              // the sequence's chunks
-  int first, last;      // the segment's chunks [first, last)
+  int first, last;      // the segment's chunks [first, last); replayed ones before it included
+  int skip;             // replayed chunks
   bool head, tail;      // first and last of its sequence in walk order
 
   // Heads that share q and k, and the value tiles of a head, go to one XCD (workgroups are
@@ -313,6 +314,8 @@ struct Chain {
     if (sg >= nsg) return false;
     first = sg * w.L;
     last = min(nch, first + w.L);
+    skip = w.replay ? first : 0;
+    first -= skip;
     head = rev ? sg == nsg - 1 : sg == 0;
     tail = rev ? sg == 0 : sg == nsg - 1;
     return true;

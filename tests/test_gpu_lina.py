@@ -99,13 +99,13 @@ def test_forward(T, dk, dv, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("B,T,Hk,H", [(1, 777, 1, 1), (1, 1500, 1, 3), (3, 1025, 2, 2), (1, 64 * 33 + 1, 2, 8)])
+@pytest.mark.parametrize("B,T,Hk,H", [(1, 129, 1, 2), (2, 511, 2, 4), (1, 777, 1, 1), (1, 1500, 1, 3), (3, 1025, 2, 2), (1, 64 * 33 + 1, 2, 8)])
 def test_forward_in_segments(B, T, Hk, H, dtype):
     """Few chains: walked in segments, the last one and its last chunk partial."""
     _check_fwd(B, T, Hk, H, 128 if H < 8 else 64, 64, dtype, seed=T)
 
 
-@pytest.mark.parametrize("B,T,Hk,H,packed", [(1, 1500, 1, 3, False), (2, 4096, 32, 64, False), (1, 5000, 4, 8, True)])
+@pytest.mark.parametrize("B,T,Hk,H,packed", [(1, 200, 1, 3, False), (1, 1500, 1, 3, False), (2, 4096, 32, 64, False), (1, 5000, 4, 8, True)])
 def test_state_in_place_over_segments(B, T, Hk, H, packed):
     """final_state may be initial_state: a segment that ends early must not be read as the start."""
     import torch
@@ -144,15 +144,16 @@ def test_forward_decays(kind, dtype):
     _check_fwd(1, 1100, 1, 1, 128, 64, dtype, seed=4, g=_decays(kind, 1, 1100, 1))
 
 
+@pytest.mark.parametrize("cu,T,place", [([0, 0, 1, 65, 65, 129, 900, 1000, 1000], 1020, True),
+                                        ([0, 1, 66, 66, 180, 180], 185, False), ([0, 63, 300, 470], 470, True)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_forward_packed(dtype):
+def test_forward_packed(dtype, cu, T, place):
     """Ragged lengths with empty sequences at both ends and inside, tokens behind the last one
-    left as they were, the state in place."""
+    left as they were, the state in place or not."""
     import torch
 
     import gated_delta_rule_78_amd as kda
-    cu = [0, 0, 1, 65, 65, 129, 900, 1000, 1000]
-    T, Hk, H, dk, dv = 1020, 1, 2, 128, 64
+    Hk, H, dk, dv = 1, 2, 128, 64
     n = len(cu) - 1
     q, k, v, g, _ = _inputs(1, T, Hk, H, dk, dv, dtype, seed=8)
     S0 = torch.randn(n, H, dk, dv, generator=torch.Generator().manual_seed(2))
@@ -160,10 +161,10 @@ def test_forward_packed(dtype):
     for x in (qd, kd, vd):
         x[:, cu[-1]:] = float("nan")
     out = torch.full((1, T, H, dv), 7.0, dtype=v.dtype, device="cuda")
-    o, sT = kda.lina_chunk_fwd(qd, kd, vd, gd, initial_state=S, final_state=S, out=out,
+    o, sT = kda.lina_chunk_fwd(qd, kd, vd, gd, initial_state=S, final_state=S if place else None, out=out,
                                cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
-    assert o is out and sT is S and bool((o[:, cu[-1]:] == 7.0).all())
+    assert o is out and (sT is S) == place and bool((o[:, cu[-1]:] == 7.0).all())
     rs = ref.packed(cu, ref.lina_fwd, _np(q), _np(k), _np(v), _np(g), states=(_np(S0),))
     ra = ref.packed(cu, ref.lina_fwd, *(np.abs(_np(x)) for x in (q, k, v)), _np(g), states=(np.abs(_np(S0)),))
     for i, (lo, hi) in enumerate(zip(cu, cu[1:])):
