@@ -170,12 +170,16 @@ def _torch():
 
 
 def _dtype_code(t) -> int:
+    return _dtype_code_of(t.dtype)
+
+
+def _dtype_code_of(dtype) -> int:
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return F32
-    raise TypeError(f"q/k/v/alpha/beta must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"q/k/v/alpha/beta must be bfloat16 or float32, got {dtype}")
 
 
 def _check(ts, names, dev):

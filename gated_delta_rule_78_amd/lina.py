@@ -15,9 +15,28 @@ import gated_delta_rule_78_amd as _kda
 
 
 @functools.lru_cache(maxsize=1024)
-def _sized(B, T, Hk, H, dk, dv, code, n, bwd):
-    """(the C shape, bytes of workspace); n: sequences of a packed batch, or -1."""
-    shape = _kda.Shape(B, T, H, dk, dv, 64, code)
+def _plan(q, k, v, log_decay, n, bwd):
+    """Checks shared by every form, once for the sizes they look at.  q, k, v, log_decay: (shape, dtype);
+    n: sequences of a packed batch, or -1.  Returns (Hk, H, dk, dv, per_head, C shape, bytes of workspace)."""
+    torch = _kda._torch()
+    (qs, dtype), (vs, vt) = q, v
+    lead = tuple(qs[:-2])
+    if len(qs) not in (3, 4) or len(vs) != len(qs):
+        raise ValueError("q, k, v are [B,T,heads,channels], or [B,heads,channels] for one token")
+    Hk, dk = qs[-2:]
+    H, dv = vs[-2:]
+    code = _kda._dtype_code_of(dtype)
+    for t, nm in ((k[1], "k"), (vt, "v")):
+        if t != dtype:
+            raise TypeError(f"{nm} must have the dtype of q")
+    if k[0] != qs or tuple(vs[:-2]) != lead or Hk < 1 or H % max(Hk, 1) != 0:
+        raise ValueError("shapes: q, k [..., Hk, dk]; v [..., H, dv] with H a multiple of Hk")
+    if log_decay[1] != torch.float32:
+        raise TypeError("log_decay must be float32")
+    per_head = len(log_decay[0]) == 1
+    if tuple(log_decay[0]) != ((H,) if per_head else (*lead, H)):
+        raise ValueError("log_decay: [..., H] as v, or [H]")
+    shape = _kda.Shape(lead[0], lead[1] if len(lead) > 1 else 1, H, dk, dv, 64, code)
     ref = ctypes.byref(shape)
     L = _kda.lib()
     if bwd:
@@ -26,29 +45,11 @@ def _sized(B, T, Hk, H, dk, dv, code, n, bwd):
     else:
         need = L.kda_lina_chunk_fwd_workspace_size(ref) if n < 0 else \
             L.kda_lina_chunk_fwd_varlen_workspace_size(ref, n)
-    return shape, int(need)
+    return Hk, H, dk, dv, per_head, shape, int(need)
 
 
-def _operands(q, k, v, log_decay, lead):
-    """Checks shared by every form; lead: the shape before the heads.  Returns (Hk, H, dk, dv, code, per_head)."""
-    torch = _kda._torch()
-    n = len(lead)
-    if q.dim() != n + 2 or v.dim() != n + 2:
-        raise ValueError(f"q, k, v have {n + 2} dimensions")
-    Hk, dk = q.shape[-2:]
-    H, dv = v.shape[-2:]
-    code = _kda._dtype_code(q)
-    for t, nm in ((k, "k"), (v, "v")):
-        if t.dtype != q.dtype:
-            raise TypeError(f"{nm} must have the dtype of q")
-    if k.shape != q.shape or v.shape != (*lead, H, dv) or Hk < 1 or H % max(Hk, 1) != 0:
-        raise ValueError("shapes: q, k [..., Hk, dk]; v [..., H, dv] with H a multiple of Hk")
-    if log_decay.dtype != torch.float32:
-        raise TypeError("log_decay must be float32")
-    per_head = log_decay.dim() == 1
-    if log_decay.shape != ((H,) if per_head else (*lead, H)):
-        raise ValueError("log_decay: [..., H] as v, or [H]")
-    return Hk, H, dk, dv, code, per_head
+def _planned(q, k, v, log_decay, n=-1, bwd=False):
+    return _plan((q.shape, q.dtype), (k.shape, k.dtype), (v.shape, v.dtype), (log_decay.shape, log_decay.dtype), n, bwd)
 
 
 def _states(ts, n, H, dk, dv):
@@ -58,11 +59,13 @@ def _states(ts, n, H, dk, dv):
             raise ValueError(f"{nm} must be float32 [{n},{H},{dk},{dv}]")
 
 
-def _packed(cu_seqlens, B):
+def _sequences(q, cu_seqlens):
     torch = _kda._torch()
+    if q.dim() != 4:
+        raise ValueError("q, k are [B,T,heads,channels]")
     if cu_seqlens is None:
-        return B
-    if B != 1:
+        return q.shape[0]
+    if q.shape[0] != 1:
         raise ValueError("a packed batch has B == 1")
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise TypeError("cu_seqlens must be a 1-D int32 tensor")
@@ -87,18 +90,16 @@ def lina_chunk_fwd(q, k, v, log_decay, initial_state=None, out=None, final_state
     None)."""
     torch = _kda._torch()
     q, k = _kda._prepared(q, k, qk_prep)
-    B, T = q.shape[:2]
-    Hk, H, dk, dv, code, per_head = _operands(q, k, v, log_decay, (B, T))
-    n = _packed(cu_seqlens, B)
+    n = _sequences(q, cu_seqlens)
+    Hk, H, dk, dv, per_head, shape, need = _planned(q, k, v, log_decay, -1 if cu_seqlens is None else n)
     dev = q.device
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
-    elif out.dtype != q.dtype or out.shape != (B, T, H, dv):
+        out = torch.empty(v.shape, dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.shape != v.shape:
         raise ValueError("out must be [B,T,H,dv] in the dtype of q")
     if final_state is None and want_final:
         final_state = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
     _states(((initial_state, "initial_state"), (final_state, "final_state")), n, H, dk, dv)
-    shape, need = _sized(B, T, Hk, H, dk, dv, code, -1 if cu_seqlens is None else n, False)
     workspace, nbytes = _workspace(need, workspace, dev)
     _kda._check((q, k, v, log_decay, cu_seqlens, initial_state, out, final_state, workspace),
                 ("q", "k", "v", "log_decay", "cu_seqlens", "initial_state", "out", "final_state", "workspace"), dev)
@@ -120,18 +121,16 @@ def lina_chunk_bwd(q, k, v, log_decay, d_o, initial_state=None, d_final_state=No
     get the sum), d_log_decay fp32 in the shape of log_decay, d_initial_state fp32.  Tokens of a
     packed batch after the last offset get zeros."""
     torch = _kda._torch()
-    B, T = q.shape[:2]
-    Hk, H, dk, dv, code, per_head = _operands(q, k, v, log_decay, (B, T))
+    n = _sequences(q, cu_seqlens)
+    Hk, H, dk, dv, per_head, shape, need = _planned(q, k, v, log_decay, -1 if cu_seqlens is None else n, True)
     if d_o.dtype != q.dtype or d_o.shape != v.shape:
         raise ValueError("d_o must be [B,T,H,dv] in the dtype of q")
-    n = _packed(cu_seqlens, B)
     _states(((initial_state, "initial_state"), (d_final_state, "d_final_state")), n, H, dk, dv)
     dev = q.device
     new = torch.zeros_like if cu_seqlens is not None else torch.empty_like
     gq, gk, gv = new(q), new(k), new(v)
     gd = new(log_decay) if want_d_decay else None
     gs = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev) if want_d_initial else None
-    shape, need = _sized(B, T, Hk, H, dk, dv, code, -1 if cu_seqlens is None else n, True)
     workspace, nbytes = _workspace(need, workspace, dev)
     _kda._check((q, k, v, log_decay, d_o, cu_seqlens, initial_state, d_final_state, workspace),
                 ("q", "k", "v", "log_decay", "d_o", "cu_seqlens", "initial_state", "d_final_state", "workspace"), dev)
@@ -145,11 +144,12 @@ def lina_chunk_bwd(q, k, v, log_decay, d_o, initial_state=None, d_final_state=No
     return gq, gk, gv, gd, gs
 
 
-def _decode(entry, q, k, v, log_decay, state, out, lead):
+def _decode(entry, q, k, v, log_decay, state, out, dims):
     torch = _kda._torch()
-    Hk, H, dk, dv, code, per_head = _operands(q, k, v, log_decay, lead)
-    B, T = lead[0], lead[1] if len(lead) > 1 else 1
-    _states(((state, "state"),), B, H, dk, dv)
+    if q.dim() != dims:
+        raise ValueError(f"q, k, v have {dims} dimensions")
+    Hk, H, dk, dv, per_head, shape, _ = _planned(q, k, v, log_decay)
+    _states(((state, "state"),), q.shape[0], H, dk, dv)
     dev = q.device
     if out is None:
         out = torch.empty_like(v)
@@ -157,7 +157,6 @@ def _decode(entry, q, k, v, log_decay, state, out, lead):
         raise ValueError("out must have the shape of v and the dtype of q")
     _kda._check((q, k, v, log_decay, state, out), ("q", "k", "v", "log_decay", "state", "out"), dev)
     p = _kda._addr
-    shape, _ = _sized(B, T, Hk, H, dk, dv, code, -1, False)
     _kda._launch(entry, dev, ctypes.byref(shape), Hk, p(q), p(k), p(v), p(log_decay), per_head, p(state), p(out))
     return out
 
@@ -166,7 +165,7 @@ def lina_decode_step(q, k, v, log_decay, state, out=None, qk_prep=None):
     """One recurrent token for every (b, h): q, k [B,Hk,dk]; v [B,H,dv]; log_decay fp32 [B,H] or
     [H]; state fp32 [B,H,dk,dv] updated in place; qk_prep as lina_chunk_fwd.  Returns o [B,H,dv]."""
     q, k = _kda._prepared(q, k, qk_prep)
-    return _decode("kda_lina_decode_step", q, k, v, log_decay, state, out, tuple(q.shape[:1]))
+    return _decode("kda_lina_decode_step", q, k, v, log_decay, state, out, 3)
 
 
 def lina_decode_tokens(q, k, v, log_decay, state, out=None, qk_prep=None):
@@ -174,4 +173,4 @@ def lina_decode_tokens(q, k, v, log_decay, state, out=None, qk_prep=None):
     v [B,T,H,dv]; log_decay fp32 [B,T,H] or [H]; state fp32 [B,H,dk,dv] in place.
     qk_prep as lina_chunk_fwd.  Returns o [B,T,H,dv]."""
     q, k = _kda._prepared(q, k, qk_prep)
-    return _decode("kda_lina_decode_tokens", q, k, v, log_decay, state, out, tuple(q.shape[:2]))
+    return _decode("kda_lina_decode_tokens", q, k, v, log_decay, state, out, 4)

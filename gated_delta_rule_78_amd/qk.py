@@ -10,6 +10,7 @@ axes.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import gated_delta_rule_78_amd as _kda
 
@@ -25,20 +26,15 @@ def rope_inv_freq(rotary_dim, base=10000.0, device="cuda"):
     return (float(base) ** (-2.0 * c / rotary_dim)).to(device)
 
 
-def _tokens(x, nm, dev):
-    """(stride between tokens, dense) of [B,T,H,d] or [B,H,d] whose rows of a token are dense."""
-    if not x.is_cuda or x.device != dev:
-        raise ValueError(f"{nm} must be on {dev}")
-    H, d = x.shape[-2:]
-    dense = H * d
-    if x.is_contiguous():
-        return dense, True
-    lead = x.shape[:-2]
-    if x.stride(-1) != 1 or (H > 1 and x.stride(-2) != d):
+def _step(shape, stride, nm):
+    """Elements between tokens of [B,T,H,d] or [B,H,d] whose rows of a token are dense."""
+    H, d = shape[-2:]
+    if 0 in shape:
+        return H * d
+    if (d > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != d):
         raise ValueError(f"{nm}: the heads of a token must lie back to back")
-    step = None
-    expect = None
-    for n, st in zip(reversed(lead), reversed(x.stride()[:-2])):
+    step = expect = None
+    for n, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if n == 1:
             continue
         if step is None:
@@ -46,52 +42,68 @@ def _tokens(x, nm, dev):
         if st != expect:
             raise ValueError(f"{nm}: tokens must be evenly spaced")
         expect = st * n
-    step = dense if step is None else step
-    if step < dense:
+    step = H * d if step is None else step
+    if step < H * d:
         raise ValueError(f"{nm}: tokens must not overlap")
-    return step, step == dense
+    return step
 
 
-def _shape(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interleaved):
+@functools.lru_cache(maxsize=1024)
+def _shape(q, k, norm, eps, weight_offset, freqs, positions, sections, interleaved):
+    """(the C shape, bytes of the backward's workspace) of a call with these sizes, once checked.
+    q, k: (shape, stride, dtype) or None; freqs, positions: (shape, dtype) or None."""
     torch = _kda._torch()
     if norm not in _NORMS:
         raise ValueError(f"unknown norm {norm!r}")
-    if q.dim() not in (3, 4):
+    (qs, qt, dtype) = q
+    if len(qs) not in (3, 4):
         raise ValueError("q: [B,T,H,d] or [B,H,d]")
-    lead, (Hq, d) = tuple(q.shape[:-2]), q.shape[-2:]
+    lead, (Hq, d) = tuple(qs[:-2]), qs[-2:]
     if k is not None:
-        if k.dtype != q.dtype:
+        if k[2] != dtype:
             raise TypeError("k must have the dtype of q")
-        if k.dim() != q.dim() or tuple(k.shape[:-2]) != lead or k.shape[-1] != d:
+        if len(k[0]) != len(qs) or tuple(k[0][:-2]) != lead or k[0][-1] != d:
             raise ValueError("shapes: q [..., Hq, d]; k [..., Hk, d]")
-    dev = q.device
     n = lead[0] if len(lead) == 1 else lead[0] * lead[1]
-    s = _kda.QkShape(tokens=n, q_heads=Hq, k_heads=0 if k is None else k.shape[-2], d=d, norm=_NORMS[norm],
+    s = _kda.QkShape(tokens=n, q_heads=Hq, k_heads=0 if k is None else k[0][-2], d=d, norm=_NORMS[norm],
                      eps=float(eps), weight_offset=float(weight_offset), interleaved=int(bool(interleaved)),
-                     dtype=_kda._dtype_code(q))
-    s.q_stride, dense_q = _tokens(q, "q", dev)
-    s.k_stride, dense_k = _tokens(k, "k", dev) if k is not None else (0, True)
-    if (inv_freq is None) != (positions is None):
+                     dtype=_kda._dtype_code_of(dtype))
+    s.q_stride = _step(qs, qt, "q")
+    s.k_stride = 0 if k is None else _step(k[0], k[1], "k")
+    if (freqs is None) != (positions is None):
         raise ValueError("inv_freq and positions go together")
-    if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+    if freqs is not None:
+        if freqs[1] != torch.float64 or len(freqs[0]) != 1:
             raise TypeError("inv_freq must be a 1-D float64 tensor (rope_inv_freq makes one)")
-        if positions.dtype not in (torch.int32, torch.int64):
+        if positions[1] not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64")
-        half = inv_freq.numel()
+        half = freqs[0][0]
         sec = [half] if sections is None else [int(x) for x in sections]
         if not 1 <= len(sec) <= 4 or min(sec) < 0 or sum(sec) != half:
             raise ValueError("sections: up to four counts of frequencies that add up to inv_freq's")
         want = lead if sections is None else (len(sec), *lead)
-        if tuple(positions.shape) != want:
+        if tuple(positions[0]) != want:
             raise ValueError(f"positions must have the shape {list(want)}")
-        s.rotary_dim, s.n_axes, s.positions_64 = 2 * half, len(sec), int(positions.dtype == torch.int64)
+        s.rotary_dim, s.n_axes, s.positions_64 = 2 * half, len(sec), int(positions[1] == torch.int64)
         for i, x in enumerate(sec):
             s.sections[i] = x
-        _kda._check((inv_freq, positions), ("inv_freq", "positions"), dev)
     elif sections is not None:
         raise ValueError("sections need inv_freq and positions")
-    return s, dev, dense_q, dense_k
+    return s, int(_kda.lib().kda_qk_norm_rope_bwd_workspace_size(ctypes.byref(s)))
+
+
+def _call(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interleaved):
+    """_shape of these tensors, which have to be on q's device."""
+    dev = q.device
+    for x, nm in ((q, "q"), (k, "k")):
+        if x is not None and (not x.is_cuda or x.device != dev):
+            raise ValueError(f"{nm} must be on {dev}")
+    _kda._check((inv_freq, positions), ("inv_freq", "positions"), dev)
+    s, need = _shape((q.shape, q.stride(), q.dtype), None if k is None else (k.shape, k.stride(), k.dtype), norm, eps,
+                     weight_offset, None if inv_freq is None else (inv_freq.shape, inv_freq.dtype),
+                     None if positions is None else (positions.shape, positions.dtype),
+                     None if sections is None else tuple(sections), bool(interleaved))
+    return s, need, dev
 
 
 def _weights(ws, d, dev):
@@ -126,7 +138,7 @@ def qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps=1e-
     [B]); with sections = (n_0, n_1, ...): [axes,B,T], the first n_0 frequencies turned by axis
     0, and so on.  interleaved: pairs (2c, 2c+1) instead of (c, c + rotary_dim / 2).
     q_out, k_out may be q and k themselves where these are contiguous.  Returns (q', k')."""
-    s, dev, _, _ = _shape(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interleaved)
+    s, _, dev = _call(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interleaved)
     _weights(((q_weight, "q_weight"), (k_weight, "k_weight")), q.shape[-1], dev)
     q_out, k_out = _like(q_out, q, "q_out", dev), _like(k_out, k, "k_out", dev)
     p = _kda._addr
@@ -141,7 +153,7 @@ def qk_norm_rope_bwd(d_q, d_k, q, k=None, *, norm="rms", q_weight=None, k_weight
     of q, k), the rest its arguments.  Returns (dq, dk, d_q_weight, d_k_weight); the weights'
     gradients are fp32, None where there is no weight."""
     torch = _kda._torch()
-    s, dev, _, _ = _shape(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interleaved)
+    s, need, dev = _call(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interleaved)
     if (d_k is None) != (k is None):
         raise ValueError("d_k and k go together")
     for g, x, nm in ((d_q, q, "d_q"), (d_k, k, "d_k")):
@@ -153,8 +165,8 @@ def qk_norm_rope_bwd(d_q, d_k, q, k=None, *, norm="rms", q_weight=None, k_weight
     gq, gk = _like(None, q, "dq", dev), _like(None, k, "dk", dev)
     gwq = torch.empty_like(q_weight) if q_weight is not None else None
     gwk = torch.empty_like(k_weight) if k_weight is not None else None
-    need = int(_kda.lib().kda_qk_norm_rope_bwd_workspace_size(ctypes.byref(s))) if q_weight is not None or \
-        k_weight is not None else 0
+    if q_weight is None and k_weight is None:
+        need = 0
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
