@@ -33,12 +33,12 @@ struct LinaWalk {
   float* seg_state = nullptr; // [segments][H][dv / 64][dk * 64]
   float* seg_dec = nullptr;   // [segments][H]
   // batch
-  const int* cs = nullptr;    // clamped offsets of a packed batch [n + 1], or NULL
+  const int* cs = nullptr;    // clamped offsets of a packed batch [n + 1] and its chunks of a segment, or NULL
   const int* list = nullptr;  // its segments in the order they are dealt, [slots][2]
   int n = 0;                  // sequences
   int T = 0;                  // tokens of each sequence (packed: of the batch)
   int H = 0, dk = 0, dv = 0;  // the walk's own widths: Q, K have dk channels, V, out dv
-  int L = 0;                  // chunks of a segment
+  int L = 0;                  // chunks of a segment (packed: the least)
   bool split = false;         // segments are walked apart (L < the longest chain)
   bool replay = false;        // forward: a segment's state from all chunks before it, by itself
   bool bf16 = true;
@@ -61,7 +61,8 @@ hipError_t launch_lina_walk(const LinaWalk& w);
 hipError_t launch_lina_pair(const LinaWalk& wq, const LinaWalk& wv);
 // dk's and dv's walk in one kernel: bf16, widths equal; wv.x: v
 hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv);
-hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream);
+// chains: of a sequence
+hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int chains, int* cs, int* list, void* stream);
 hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int heads, int group, int d, bool bf16,
                                const int* end, void* stream);
 hipError_t launch_lina_ddecay(const LinaWalk& w, const float* a, const float* b, const float* e, int na, int ne,

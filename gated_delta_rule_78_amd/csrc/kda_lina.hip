@@ -20,9 +20,9 @@
 //   kLinaGroup chunks it is taken afresh from the two states, so that no rounding error
 //   travels further than that.
 //
-// One workgroup of four waves walks one chain (sequence or segment, head, 64 value columns);
-// wave w keeps columns 16 w .. 16 w + 15 of the state in fp32 accumulators, which serve as
-// matrix-core operands without leaving the registers.  Products run transposed (rows are
+// Four waves walk one chain (sequence or segment, head, 64 value columns) or keep its state beside
+// others that feed them; wave w keeps columns 16 w .. 16 w + 15 of the state in fp32 accumulators,
+// which serve as matrix-core operands without leaving the registers.  Products run transposed (rows are
 // value columns, columns are tokens), so that a lane holds four neighbouring columns of one
 // token and stores them at once; K and V are read along the token axis with the LDS
 // transpose loads.
@@ -45,8 +45,13 @@ namespace {
 
 // bf16: eight waves, two to a SIMD, one barrier per chunk.  Waves 0-3 keep the state and make
 // the outputs of chunk c; waves 4-7 meanwhile write the tiles of chunk c + 2 to LDS (fetched two
-// steps before, into the one of two register sets that is free), compute its decays, and make P of chunk c + 1, so that neither the fetch nor
-// Q K^T lies on the state's path.  Tiles are triple-, P double-buffered.
+// steps before, into the one of two register sets that is free), compute its decays, and make P of
+// chunk c + 1, so that neither the fetch nor Q K^T lies on the state's path.  Tiles are triple-, P
+// double-buffered.  B4 H32 T8K, d = 128 (256 chains, one to a compute unit): 290 us, 3.8 TB/s of the
+// bytes that have to move (copies: 5.15).  Loads and stores of the same pattern with no arithmetic take
+// 234 us; a step is 4,800 cycles, matrix cores busy 27% and vector units 44% of them, at the 1.75 GHz
+// that the clock settles at.  With all work in four waves it took 450 us, with twelve waves (fetch and
+// P apart) 300.
 template <int DK, int DOT>
 struct PipeLds {
   static constexpr int TILES = 2 * Tile<bf16_t, DK>::BYTES + Tile<bf16_t, VT>::BYTES;
@@ -199,7 +204,9 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
 // transposed state and make dk, four 64 columns of the state and make dv, four fetch, write and
 // make the scores of the next chunk.  A step has two halves: from the states (meanwhile the next
 // tiles and this chunk's P go to LDS), then P V and the states' update (meanwhile the next scores,
-// kept in registers).  With separate walks B4 H32 T8K took 0.87 ms here.
+// kept in registers).  B4 H32 T8K, d = 128: 650 to 700 us (with the clock), 11,900 cycles a step, of
+// which the vector units are busy 46% and the matrix cores 26%: the two chains of dependent products
+// between two barriers, not memory (1.75 GB).  Two separate walks took 870.
 template <int D>
 struct RevLds {
   static constexpr int Q = 0, K = Tile<bf16_t, D>::BYTES, V = 2 * K, U = 3 * K, TILES = 4 * K;
@@ -400,7 +407,9 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
   }
 }
 
-// fp32: one workgroup of four waves, one tile buffer, chunk after chunk.
+// fp32: one workgroup of four waves, one tile buffer, chunk after chunk; products of 16 x 16 x 4 at
+// 32 cycles each.  d = 64: 11 us for a chain's first chunk (latency of its loads and products), 5 for
+// each further one; chains are therefore cut to single chunks while there are compute units to spare.
 template <int DK, bool REV, int DOT>
 __device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned block) {
   typedef float T;
@@ -498,7 +507,8 @@ __global__ __launch_bounds__(NT) void lina_walk_f32_kernel(const WalkParams p) {
 }
 
 // The walks of dq and dv side by side: they need nothing of each other, and fp32 calls are seldom
-// large enough to fill the machine with one.
+// large enough to fill the machine with one (2 x 1,001 tokens, H4, d = 64: 19 us for both, 17 for
+// one).
 struct PairParams {
   WalkParams q, v;
   unsigned blocks_q;
@@ -512,7 +522,9 @@ __global__ __launch_bounds__(NT) void lina_pair_f32_kernel(const PairParams p) {
 
 // End states of the segments from a zero start: the walk without its outputs.  Two tile
 // buffers, one barrier per chunk; small enough for three workgroups on a compute unit.  Walks of one
-// call that have d_k in common (the backward's three) go in one launch.
+// call that have d_k in common (the backward's three) go in one launch.  H16 T128K, d = 128: 310 us for
+// 1.07 GB of k and v (3.5 TB/s; matrix cores busy 27%, vector units 44%); with tiles fetched three
+// chunks ahead instead of two 300 there, but 235 instead of 219 us for a backward of H4 T32K.
 struct SegParams {
   WalkParams p[3];
   unsigned end[3];  // their workgroups, running sums
@@ -648,15 +660,20 @@ WalkParams walk_params(const LinaWalk& w) {
   return p;
 }
 
-// Packed offsets clamped to [0, T] and made non-decreasing (a running maximum), cs[0] = 0, and
-// the list of segments (sequence, segment), the longest first (in 64 classes): workgroups are
-// dealt in that order, so that no long chain starts last.  Order within a class is left to
-// chance; no result depends on it.  Slots that no segment needs hold -1.
+// Packed offsets clamped to [0, T] and made non-decreasing (a running maximum), cs[0] = 0; the
+// chunks of a segment, cs[n + 1]; and the list of segments (sequence, segment), the longest first
+// (in 64 classes): workgroups are dealt in that order, so that no long chain starts last.  Order
+// within a class is left to chance; no result depends on it.  Slots that no segment needs hold -1.
+//
+// Only here are the lengths known.  Whole chains take the longest one's steps or a compute unit's
+// share of all steps, whichever is more; segments of `least` chunks that share and half of it again
+// (their end states come first).  Prompts of 20,011 tokens, H = 32, d = 128, one of them 0.44 of all
+// (1.7 shares): 308 us whole, 281 cut; 0.6 of all (2.2 shares): 369 and 291; 24 like ones: 218 whole.
 constexpr int NTB = 1024;
-__global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T, int L,
-                                                           int64_t slots, int* __restrict__ cs,
+__global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T, int least,
+                                                           int chains, int64_t slots, int* __restrict__ cs,
                                                            int* __restrict__ list) {
-  __shared__ int part[NTB], from[64];
+  __shared__ int part[NTB], from[64], total, longest;
   const int tid = threadIdx.x, per = (nseq + NTB - 1) / NTB;
   const int s0 = min(nseq, tid * per), s1 = min(nseq, s0 + per);
   int mx = 0;
@@ -671,9 +688,10 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
   }
   const int run0 = tid ? part[tid - 1] : 0;
   if (tid < 64) from[tid] = 0;
-  if (tid == 0) cs[0] = 0;
+  if (tid == 0) cs[0] = total = longest = 0;
   __syncthreads();
-  auto each = [&](auto fn) {  // this thread's segments
+  int L = 1;
+  auto each = [&](auto fn) {  // this thread's sequences
     int run = run0;
     for (int i = s0; i < s1; ++i) {
       const int end = max(run, min(max(cu[i + 1], 0), T));
@@ -682,6 +700,18 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
       run = end;
     }
   };
+  int sum = 0, top = 0;
+  each([&](int, int, int nch, int) {
+    sum += nch;
+    top = max(top, nch);
+  });
+  if (top > 0) {
+    atomicAdd(&total, sum);
+    atomicMax(&longest, top);
+  }
+  __syncthreads();
+  L = (int64_t)longest * 160 > (int64_t)total * chains ? least : max(least, longest);  // 1.6 shares of 256
+  if (tid == 0) cs[nseq + 1] = L;
   auto cls = [&](int len) { return 63 - (int)((int64_t)len * 63 / L); };
   each([&](int i, int end, int nch, int nsg) {
     cs[i + 1] = end;
@@ -736,7 +766,7 @@ __global__ __launch_bounds__(256) void lina_headsum_kernel(const float* __restri
 }
 
 // dg from the walks' parts: one workgroup of 16 waves per group of 16 chunks and head,
-// wave = chunk, lane = token
+// wave = chunk, lane = token.  B4 H32 T8K: 20 us; sums in fp64, so that none of its roundings counts.
 __global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const int* __restrict__ cs, int nseq, int T, int H,
                                                            int64_t rows, const float* __restrict__ a,
                                                            const float* __restrict__ b, const float* __restrict__ e,
@@ -876,8 +906,8 @@ hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv) {
   return want ? reverse<64, true>(p) : reverse<64, false>(p);
 }
 
-hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int* cs, int* list, void* stream) {
-  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, L,
+hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int chains, int* cs, int* list, void* stream) {
+  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, L, chains,
                      lina_pieces(T, n, L), cs, list);
   return hipGetLastError();
 }

@@ -50,15 +50,15 @@ int segment_override() {
 // units it is cut into segments of L chunks, whose start states cost one more read of k and v
 // (the segments' end states first, then every segment from its own start).  Measured, bf16,
 // d = 128, forward: with 256 chains or more whole chains win; below, one segment per compute
-// unit (work / 256: 512 chunks of 8 chains 79 us at L = 16, 93 at 8, 96 at 24), or two where
-// segments stay long, for the sake of the first pass (128 chunks of 64 chains 131 us at L = 16,
-// 137 at 32, 245 whole; 2,048 of 32 chains 931 at 128, 991 at 256).  Short segments
+// unit (work / 256: 512 chunks of 8 chains 81 us at L = 16, 90 at 8, 102 at 24), or two where
+// segments stay long, for the sake of the first pass (128 chunks of 64 chains 120 us at L = 16,
+// 131 at 32, 235 whole; 2,048 of 32 chains 875 at 128, 953 at 256, 3,642 whole).  Short segments
 // cost their successors a state to add, nch / L of them in a row: with a step of s and an
-// addition of f, 2 L s + f nch / L is least at L = sqrt(nch f / 2 s) (64 chunks of 8 chains: 30 us
-// at L = 3, 53 at 1, 63 at 16; fp32, 16 chunks: 25 us at 1, 45 at 4, 107 whole).  Packed chains
-// are dealt longest first; 256 or more are cut only where one alone would take twice as long as
-// all of them spread evenly (6 prompts of 20,011 tokens, H = 32: 241 us whole, 331 at L = 80; 24:
-// 217 and 262).
+// addition of f, 2 L s + f nch / L is least at L = sqrt(nch f / 2 s) (64 chunks of 8 chains: 29 us
+// at L = 3, 50 at 1, 68 at 16; fp32, 16 chunks: 22.5 us at 1, 46 at 4, 109 whole).  Packed chains
+// are cut, or not, where their lengths are known (lina_offsets_kernel): L is the least that their
+// segments may have, and half a compute unit's share of the steps is right where one chain is long
+// (24 prompts of 20,011 tokens, H = 32, one 0.6 of all: 291 us at 40, half the share; 356 at 80).
 // Of the shortest chains every segment makes its start state itself, from the chunks before it,
 // which saves the first pass and its launch: bf16, 8 heads, d = 128: 3 chunks 10.3 us against
 // 12.9, 8 chunks 16.8 and 17.4, 10 chunks 19.1 and 17.6; fp32, whose steps are dearer, 4 heads,
@@ -72,8 +72,7 @@ Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
   int64_t L = nch;
   if (packed || chains < 256) {
     L = (work + 255) / 256;
-    if (chains >= 256) L *= 2;
-    else if (L >= 32) L = (work + 511) / 512;
+    if (chains >= 256 || L >= 32) L = (work + 511) / 512;
     L = std::max<int64_t>(L, (int64_t)std::ceil(std::sqrt((double)nch * (s.dtype == KDA_BF16 ? 0.16 : 0.06))));
   }
   if (segment_override() > 0) L = segment_override();
@@ -102,7 +101,7 @@ FwdLayout fwd_layout(const kda_shape& s, int n_seqs) {
   const size_t seg = l.plan.split && !l.plan.replay ? (size_t)l.plan.nseg : 0;
   l.off_dec = up(seg * s.H * s.dk * s.dv * 4);
   l.off_cs = up(l.off_dec + seg * s.H * 4);
-  l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
+  l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 2) * 4 : 0));
   l.bytes = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
   return l;
 }
@@ -169,8 +168,8 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
   if (packed) {
     a.cs = (const int*)(w + l.off_cs);
     a.list = (const int*)(w + l.off_list);
-    if (kda::launch_lina_offsets(cu, n_seqs, s.T, a.L, (int*)(w + l.off_cs), (int*)(w + l.off_list), stream) !=
-        hipSuccess)
+    if (kda::launch_lina_offsets(cu, n_seqs, s.T, a.L, s.H * (s.dv / 64), (int*)(w + l.off_cs),
+                                 (int*)(w + l.off_list), stream) != hipSuccess)
       return KDA_ERR_HIP;
   }
   if (kda::launch_lina_segments(&a, 1) != hipSuccess) return KDA_ERR_HIP;
@@ -198,7 +197,7 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   l.off_seg3 = up(l.off_dec2 + seg * s.H * 4);
   l.off_dec3 = up(l.off_seg3 + seg * state);
   l.off_cs = up(l.off_dec3 + seg * s.H * 4);
-  l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 1) * 4 : 0));
+  l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 2) * 4 : 0));
   l.off_snap = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
   l.off_anchor = up(l.off_snap + l.groups * state);
   l.off_a = up(l.off_anchor + (size_t)l.groups * s.H * (s.dk / 64) * 4 * 4);
@@ -280,8 +279,8 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
   if (packed) {
     a.cs = (const int*)(ws + l.off_cs);
     a.list = (const int*)(ws + l.off_list);
-    if (kda::launch_lina_offsets(cu, n_seqs, s.T, a.L, (int*)(ws + l.off_cs), (int*)(ws + l.off_list), stream) !=
-        hipSuccess)
+    if (kda::launch_lina_offsets(cu, n_seqs, s.T, a.L, s.H * (std::min(s.dk, s.dv) / 64), (int*)(ws + l.off_cs),
+                                 (int*)(ws + l.off_list), stream) != hipSuccess)
       return KDA_ERR_HIP;
   }
   const bool shared = s.H > Hk;

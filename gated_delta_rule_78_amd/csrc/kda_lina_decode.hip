@@ -91,7 +91,8 @@ __global__ __launch_bounds__(NT) void lina_decode_kernel(const LinaDecodeArgs a)
 
 // 64 columns a workgroup; 512 threads where the states come from memory, 256 where they are few
 // enough to stay in the caches (H = 32, d = 128, per step: 180 us against 189 at B = 256, 46.7
-// against 47.4 at 64, but 12.7 against 10.9 at 16 and 4.7 against 4.5 at 4).  180 us are 6.0 TB/s.
+// against 47.4 at 64, but 12.7 against 10.9 at 16 and 4.7 against 4.5 at 4).  180 us are 6.0 TB/s, the
+// rate of one buffer updated in place; with another state each time 194 us, 5.6 TB/s.
 template <typename T, int DK>
 hipError_t launch_d(const LinaDecodeArgs& a) {
   const int64_t blocks = a.BH * (a.dv / 64);

@@ -280,6 +280,7 @@ struct Chain {
   // dealt to the eight in turn), next to each other.  False: nothing to do here.
   __device__ __forceinline__ bool place(const WalkParams& p, bool rev, unsigned block) {
     const LinaWalk& w = p.w;
+    const int L = (int)uniform64(w.cs ? w.cs[w.n + 1] : w.L);
     const int qk = w.q.heads < w.k.heads ? w.q.heads : w.k.heads;
     const int hk = qk < w.v.heads ? qk : w.v.heads;
     const int share = w.H / hk * p.nv;
@@ -296,7 +297,7 @@ struct Chain {
       sg = w.list[2 * seg + 1];
       lo = w.cs[sq];
       hi = w.cs[sq + 1];
-      seg = lo / ((int64_t)C * w.L) + sq + sg;
+      seg = lo / ((int64_t)C * L) + sq + sg;
     } else {
       const int64_t per = p.nseg / w.n;
       sq = (int)(seg / per);
@@ -310,10 +311,10 @@ struct Chain {
     sq = (int)uniform64(sq);
     sg = (int)uniform64(sg);
     nch = (int)((hi - lo + C - 1) / C);
-    nsg = nch > 0 ? (nch + w.L - 1) / w.L : 1;
+    nsg = nch > 0 ? (nch + L - 1) / L : 1;
     if (sg >= nsg) return false;
-    first = sg * w.L;
-    last = min(nch, first + w.L);
+    first = sg * L;
+    last = min(nch, first + L);
     skip = w.replay ? first : 0;
     first -= skip;
     head = rev ? sg == nsg - 1 : sg == 0;

@@ -144,16 +144,18 @@ def test_forward_decays(kind, dtype):
     _check_fwd(1, 1100, 1, 1, 128, 64, dtype, seed=4, g=_decays(kind, 1, 1100, 1))
 
 
-@pytest.mark.parametrize("cu,T,place", [([0, 0, 1, 65, 65, 129, 900, 1000, 1000], 1020, True),
-                                        ([0, 1, 66, 66, 180, 180], 185, False), ([0, 63, 300, 470], 470, True)])
+@pytest.mark.parametrize("cu,T,H,place", [([0, 0, 1, 65, 65, 129, 900, 1000, 1000], 1020, 2, True),
+                                          ([0, 1, 66, 66, 180, 180], 185, 2, False), ([0, 63, 300, 470], 470, 2, True),
+                                          ([0, 330, 600, 900, 1230], 1230, 64, True),   # chains whole
+                                          ([0, 60, 1000, 1030, 1100], 1100, 64, True)])  # one cut
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_forward_packed(dtype, cu, T, place):
+def test_forward_packed(dtype, cu, T, H, place):
     """Ragged lengths with empty sequences at both ends and inside, tokens behind the last one
     left as they were, the state in place or not."""
     import torch
 
     import gated_delta_rule_78_amd as kda
-    Hk, H, dk, dv = 1, 2, 128, 64
+    Hk, dk, dv = 1, 128, 64
     n = len(cu) - 1
     q, k, v, g, _ = _inputs(1, T, Hk, H, dk, dv, dtype, seed=8)
     S0 = torch.randn(n, H, dk, dv, generator=torch.Generator().manual_seed(2))
