@@ -673,23 +673,22 @@ constexpr int NTB = 1024;
 __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T, int least,
                                                            int chains, int64_t slots, int* __restrict__ cs,
                                                            int* __restrict__ list) {
-  __shared__ int part[NTB], from[64], total, longest;
-  const int tid = threadIdx.x, per = (nseq + NTB - 1) / NTB;
+  __shared__ int part[NTB / 64], from[64], total, longest, used;
+  const int tid = threadIdx.x, lane = tid & 63, per = (nseq + NTB - 1) / NTB;
   const int s0 = min(nseq, tid * per), s1 = min(nseq, s0 + per);
   int mx = 0;
   for (int i = s0; i < s1; ++i) mx = max(mx, min(max(cu[i + 1], 0), T));
-  part[tid] = mx;
-  __syncthreads();
-  for (int off = 1; off < NTB; off <<= 1) {
-    const int v = tid >= off ? part[tid - off] : 0;
-    __syncthreads();
-    part[tid] = max(part[tid], v);
-    __syncthreads();
+  for (int off = 1; off < 64; off <<= 1) {
+    const int v = __shfl_up(mx, off);
+    if (lane >= off) mx = max(mx, v);
   }
-  const int run0 = tid ? part[tid - 1] : 0;
+  if (lane == 63) part[tid >> 6] = mx;
   if (tid < 64) from[tid] = 0;
   if (tid == 0) cs[0] = total = longest = 0;
   __syncthreads();
+  int run0 = __shfl_up(mx, 1);
+  if (lane == 0) run0 = 0;
+  for (int i = 0; i < tid >> 6; ++i) run0 = max(run0, part[i]);
   int L = 1;
   auto each = [&](auto fn) {  // this thread's sequences
     int run = run0;
@@ -719,14 +718,15 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
     atomicAdd(&from[cls(nch - (nsg - 1) * L)], 1);
   });
   __syncthreads();
-  if (tid == 0) {
-    int x = 0;
-    for (int i = 0; i < 64; ++i) {
-      const int n = from[i];
-      from[i] = x;
-      x += n;
+  if (tid < 64) {
+    const int n = from[lane];
+    int x = n;
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(x, off);
+      if (lane >= off) x += v;
     }
-    part[0] = x;
+    from[lane] = x - n;
+    if (lane == 63) used = x;
   }
   __syncthreads();
   each([&](int i, int, int nch, int nsg) {
@@ -741,7 +741,7 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
     list[2 * at] = i;
     list[2 * at + 1] = nsg - 1;
   });
-  for (int64_t x = part[0] + tid; x < slots; x += NTB) list[2 * x] = -1;
+  for (int64_t x = used + tid; x < slots; x += NTB) list[2 * x] = -1;
 }
 
 // dq, dk of heads that share them: [rows, H, d] fp32 -> [rows, heads, d], summed in order; rows
