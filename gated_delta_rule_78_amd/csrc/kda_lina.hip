@@ -408,8 +408,9 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
 }
 
 // fp32: one workgroup of four waves, one tile buffer, chunk after chunk; products of 16 x 16 x 4 at
-// 32 cycles each.  d = 64: 11 us for a chain's first chunk (latency of its loads and products), 5 for
-// each further one; chains are therefore cut to single chunks while there are compute units to spare.
+// 32 cycles each.  d = 64: 11 us for a chain's first chunk (latency of its loads and products), 6.5 for
+// each further one, 2.6 where only its state is needed; chains are therefore cut to single chunks
+// while there are compute units to spare.
 template <int DK, bool REV, int DOT>
 __device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned block) {
   typedef float T;
