@@ -523,23 +523,24 @@ __global__ __launch_bounds__(NT) void lina_pair_f32_kernel(const PairParams p) {
 
 // End states of the segments from a zero start: the walk without its outputs.  Two tile
 // buffers, one barrier per chunk; small enough for three workgroups on a compute unit.  Walks of one
-// call that have d_k in common (the backward's three) go in one launch.  H16 T128K, d = 128: 310 us for
-// 1.07 GB of k and v (3.5 TB/s; matrix cores busy 27%, vector units 44%); with tiles fetched three
-// chunks ahead instead of two 300 there, but 235 instead of 219 us for a backward of H4 T32K.
+// call that have d_k in common (the backward's three) go in one launch.  H16 T128K, d = 128: SEGUS us
+// for 1.07 GB of k and v; with a step's decays made in that step by one wave it took 310 (all others
+// waited for its prefix sums).  Held to 168 registers for the third workgroup: with 188 a backward of
+// H4 T32K took 223 us instead of 215.
 struct SegParams {
   WalkParams p[3];
   unsigned end[3];  // their workgroups, running sums
 };
 
 template <typename T, int DK>
-__global__ __launch_bounds__(NT) void lina_segment_kernel(const SegParams all) {
+__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 3 : 1) void lina_segment_kernel(const SegParams all) {
   const int which = (blockIdx.x >= all.end[0]) + (blockIdx.x >= all.end[1]);
   const WalkParams& p = all.p[which];
   const unsigned block = blockIdx.x - (which ? all.end[which - 1] : 0);
   const bool rev = p.w.rev;
   constexpr int TILES = Tile<T, DK>::BYTES + Tile<T, VT>::BYTES;
   extern __shared__ __align__(16) char smem[];
-  __shared__ Decays dec[2];
+  __shared__ ColDecays dec[8];
   const LinaWalk& w = p.w;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Chain ch;
@@ -556,14 +557,21 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const SegParams all) {
     const int c = chunk(it);
     const int64_t t = ch.lo + (int64_t)c * C;
     const uint32_t n = ch.rows(c);
-    if (wave == 0) rg = rev ? row_decay<true>(w, ch, c, lane) : row_decay<false>(w, ch, c, lane);
     rk.load(k.rows(t, n), k.step, rev, tid);
     rv.load(v.rows(t, n), v.step, rev, tid);
+  };
+  // four chunks' decays at a time, a wave each: their prefix sums would hold up every step
+  auto fetch_decays = [&](int it) {
+    it += wave;
+    if (it < steps) rg = rev ? row_decay<true>(w, ch, chunk(it), lane) : row_decay<false>(w, ch, chunk(it), lane);
+  };
+  auto decays = [&](int it) {
+    it += wave;
+    if (it < steps) chunk_decays(dec[it & 7], rg, lane);
   };
   auto put = [&](int it) {
     if (it >= steps) return;
     char* t = smem + (it & 1) * TILES;
-    if (wave == 0) chunk_decays(dec[it & 1], rg, lane);
     rk.store(t, tid);
     rv.store(t + Tile<T, DK>::BYTES, tid);
   };
@@ -571,14 +579,21 @@ __global__ __launch_bounds__(NT) void lina_segment_kernel(const SegParams all) {
 #pragma unroll
   for (int ct = 0; ct < DK / 16; ++ct) S[ct] = zero4();
   float total = 1.f;
+  fetch_decays(0);
   fetch(0);
+  decays(0);
+  fetch_decays(4);
   put(0);
   fetch(1);
   lds_barrier();
   for (int it = 0; it < steps; ++it) {
     put(it + 1);
+    if (it % 4 == 0) {
+      decays(it + 4);
+      fetch_decays(it + 8);
+    }
     fetch(it + 2);
-    const Decays& dc = dec[it & 1];
+    const ColDecays& dc = dec[it & 7];
     const char* t = smem + (it & 1) * TILES;
     Frag<T> fv[2];
     tok_frag<T, VT>(fv[0], t + Tile<T, DK>::BYTES, tok_base<T, VT, false>(lane), 16 * wave, 0, lane);
@@ -669,7 +684,7 @@ WalkParams walk_params(const LinaWalk& w) {
 // Only here are the lengths known.  Whole chains take the longest one's steps or a compute unit's
 // share of all steps, whichever is more; segments of `least` chunks that share and half of it again
 // (their end states come first).  Prompts of 20,011 tokens, H = 32, d = 128, one of them 0.44 of all
-// (1.7 shares): 308 us whole, 281 cut; 0.6 of all (2.2 shares): 369 and 291; 24 like ones: 218 whole.
+// (1.7 shares): 308 us whole, 273 cut; 0.6 of all (2.2 shares): 369 and 283; 24 like ones: 218 whole.
 constexpr int NTB = 1024;
 __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T, int least,
                                                            int chains, int64_t slots, int* __restrict__ cs,

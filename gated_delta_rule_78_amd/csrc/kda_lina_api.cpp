@@ -50,15 +50,15 @@ int segment_override() {
 // units it is cut into segments of L chunks, whose start states cost one more read of k and v
 // (the segments' end states first, then every segment from its own start).  Measured, bf16,
 // d = 128, forward: with 256 chains or more whole chains win; below, one segment per compute
-// unit (work / 256: 512 chunks of 8 chains 81 us at L = 16, 90 at 8, 102 at 24), or two where
-// segments stay long, for the sake of the first pass (128 chunks of 64 chains 120 us at L = 16,
-// 131 at 32, 235 whole; 2,048 of 32 chains 875 at 128, 953 at 256, 3,642 whole).  Short segments
+// unit (work / 256: 512 chunks of 8 chains 74 us at L = 16, 87 at 8, 90 at 24), or two where
+// segments stay long, for the sake of the first pass (128 chunks of 64 chains 115 us at L = 16,
+// 116 at 32, 234 whole; 2,048 of 32 chains 860 at 128, 889 at 256, 3,620 whole).  Short segments
 // cost their successors a state to add, nch / L of them in a row: with a step of s and an
-// addition of f, 2 L s + f nch / L is least at L = sqrt(nch f / 2 s) (64 chunks of 8 chains: 29 us
-// at L = 3, 50 at 1, 68 at 16; fp32, 16 chunks: 22.5 us at 1, 46 at 4, 109 whole).  Packed chains
+// addition of f, 2 L s + f nch / L is least at L = sqrt(nch f / 2 s) (64 chunks of 8 chains: 28 us
+// at L = 3, 51 at 1, 60 at 16; fp32, 16 chunks: 22.7 us at 1, 45 at 4, 110 whole).  Packed chains
 // are cut, or not, where their lengths are known (lina_offsets_kernel): L is the least that their
 // segments may have, and half a compute unit's share of the steps is right where one chain is long
-// (24 prompts of 20,011 tokens, H = 32, one 0.6 of all: 291 us at 40, half the share; 356 at 80).
+// (24 prompts of 20,011 tokens, H = 32, one 0.6 of all: 283 us at 42, half the share; 317 at 80).
 // Of the shortest chains every segment makes its start state itself, from the chunks before it,
 // which saves the first pass and its launch: bf16, 8 heads, d = 128: 3 chunks 10.3 us against
 // 12.9, 8 chunks 16.8 and 17.4, 10 chunks 19.1 and 17.6; fp32, whose steps are dearer, 4 heads,

@@ -241,8 +241,9 @@ struct Decays {
   float pad[3];
 };
 
-// one wave: lane r holds the log decay of row r (natural logarithm, 0 for rows past the end)
-__device__ __forceinline__ void chunk_decays(Decays& d, float gr, int lane) {
+// one wave: lane r holds the log decay of row r (natural logarithm, 0 for rows past the end);
+// returns its running sum in powers of two, and the whole chunk's
+__device__ __forceinline__ double decay_sums(float gr, int lane, double& tot) {
   const double x = (double)gr * 1.4426950408889634;
   double s = x < (double)kLeast ? (double)kLeast : x;  // NaN stays
 #pragma unroll
@@ -250,11 +251,31 @@ __device__ __forceinline__ void chunk_decays(Decays& d, float gr, int lane) {
     const double y = __shfl_up(s, off);
     if (lane >= off) s += y;
   }
-  const double tot = __shfl(s, 63);
+  tot = __shfl(s, 63);
+  return s;
+}
+
+__device__ __forceinline__ void chunk_decays(Decays& d, float gr, int lane) {
+  double tot;
+  const double s = decay_sums(gr, lane, tot);
   const float hi = rintf((float)s * 8.f) * 0.125f;
   d.hi[lane] = hi;
   d.lo[lane] = (float)(s - (double)hi);
   d.row[lane] = fast_exp2((float)s);
+  d.col[lane] = fast_exp2((float)(tot - s));
+  if (lane == 0) d.tot = fast_exp2((float)tot);
+}
+
+// What a state alone needs of them.
+struct ColDecays {
+  float col[C];
+  float tot;
+  float pad[3];
+};
+
+__device__ __forceinline__ void chunk_decays(ColDecays& d, float gr, int lane) {
+  double tot;
+  const double s = decay_sums(gr, lane, tot);
   d.col[lane] = fast_exp2((float)(tot - s));
   if (lane == 0) d.tot = fast_exp2((float)tot);
 }
@@ -589,9 +610,9 @@ __device__ __forceinline__ void add_intra(f32x4_t (&acc)[4], const Frag<T> (&fv)
 }
 
 // S <- decay S + K^T (col o V), the weighted values in three bf16 terms
-template <typename T, int DK, bool LEAN = false>
+template <typename T, int DK, bool LEAN = false, typename DEC>
 __device__ __forceinline__ void add_chunk(f32x4_t (&S)[DK / 16], const Frag<T> (&fv)[2], const char* sK,
-                                          const Decays& dc, int lane) {
+                                          const DEC& dc, int lane) {
   const int g = lane >> 4;
   const uint32_t tb = tok_base<T, DK, LEAN>(lane);
   const float tot = dc.tot;
