@@ -443,8 +443,9 @@ int kda_gdn2_decode_tokens(const kda_shape* shape, const void* q, const void* k,
  *   initial_state  : [B, H, dk, dv] fp32, or NULL for zeros
  *   final_state    : [B, H, dk, dv] fp32, or NULL (not written); may equal initial_state
  *   workspace      : kda_lina_chunk_fwd_workspace_size(shape) bytes, 256-byte aligned (0 bytes,
- *                    and NULL accepted, when the chains are walked whole; with fewer chains
- *                    than compute units it holds the end states of their segments)
+ *                    and NULL accepted, when the chains are walked whole or are very short;
+ *                    with fewer chains than compute units it holds the end states of their
+ *                    segments, for a packed batch its offsets and list of segments too)
  * Arithmetic: fp32 sums, decays and states; with bf16 inputs the products r o q.k and the state
  * as q meets it are rounded to bf16 (as o is); what is added to the state is kept to 2^-24.
  * A non-finite v_t reaches the outputs from token t on only.  Alignment: 16 bytes for q, k, v,
