@@ -1,0 +1,97 @@
+"""Linear attention's backward over several groups of kept states, at forced segment lengths and with
+whole chains of several chunks, against the fp64 references (gpu); bounds as in test_gpu_lina.
+
+The decay's gradient is taken afresh from two states every so many chunks (a group): token 1,024 and
+what follows are the second group of a sequence, whose number in a packed batch depends on where the
+sequence starts.  Calls this small are cut into segments by their own rule; KDA_LINA_SEGMENT pins the
+chunks of a segment, read once per process, so each length runs in a child process of its own.
+"""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from test_gpu_lina import _check_bwd, _dev, _inputs
+
+pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,decay", [(1100, "token"), (2100, "head")])
+def test_second_and_third_group(T, decay, dtype):
+    """Two value tiles; dk and dv in one kernel for bf16."""
+    _check_bwd(1, T, 1, 1, 128, 128, dtype, decay, seed=T)
+
+
+# two sequences of more than 1,024 tokens that start off a multiple of 1,024, with an empty one between
+CU = [0, 100, 1300, 1300, 2450, 2460]
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("bf16", 128, 64), ("f32", 64, 128), ("f32", 128, 128)])
+def test_packed_groups(dtype, dk, dv):
+    out = _check_bwd(1, 2470, 1, 2, dk, dv, dtype, cu=CU, seed=31)
+    for x in out[:4]:
+        assert bool((x[:, CU[-1]:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_whole_chains(dtype):
+    """256 chains of four chunks: none is cut."""
+    _check_bwd(2, 200, 64, 128, 64, 64, dtype, seed=17)
+
+
+CHILD = r"""
+import sys
+sys.path[:0] = [{root!r}, {here!r}]
+from test_gpu_lina import _check_bwd, _check_fwd
+from test_gpu_lina_groups import CU
+for dtype, dk, dv in (("bf16", 128, 128), ("bf16", 64, 128), ("f32", 128, 64)):
+    print(dtype, dk, dv, flush=True)
+    _check_fwd(1, 1100, 1, 2, dk, dv, dtype, seed=51)
+    _check_bwd(1, 1100, 1, 1, dk, dv, dtype, seed=52)
+    _check_bwd(1, 2470, 1, 1, dk, dv, dtype, cu=CU, seed=53)
+print("ok", flush=True)
+"""
+
+
+@pytest.mark.parametrize("L", [1, 5, 1000])
+def test_forced_segments(L):
+    """Single chunks; segments that end inside a group; chains whole."""
+    print(f"linear attention with KDA_LINA_SEGMENT={L} (child process)", flush=True)
+    env = dict(os.environ, KDA_LINA_SEGMENT=str(L))
+    r = subprocess.run([sys.executable, "-c", CHILD.format(root=ROOT, here=HERE)], env=env, cwd=ROOT,
+                       capture_output=True, text=True, timeout=110)
+    print(r.stdout[-3000:], r.stderr[-3000:], flush=True)
+    assert r.returncode == 0 and r.stdout.rstrip().endswith("ok")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_backward_bad_values(dtype, bad):
+    """A value that is not finite reaches no gradient that does not depend on it: dq_i takes u_i and the k_j, v_j
+    up to i; dk_j takes v_j, dv_j takes k_j, and both the q_i, u_i from j on."""
+    import torch
+
+    import gated_delta_rule_78_amd as kda
+    T, d = 150, 64
+    q, k, v, g, u = _dev(*_inputs(1, T, 1, 1, d, d, dtype, seed=2))
+    good = kda.lina_chunk_bwd(q, k, v, g, u)[:3]
+    names = ("q", "k", "v", "u")
+    # tokens whose dq, dk, dv may not change when x_t is bad
+    before, after, but, all_ = (lambda t: slice(0, t)), (lambda t: slice(t + 1, T)), None, (lambda t: slice(0, T))
+    clean = {"q": (all_, after, after), "k": (before, all_, but), "v": (before, but, all_), "u": (but, after, after)}
+    for t in (5, 63, 100, 149):
+        for i, name in enumerate(names):
+            x = [y.clone() for y in (q, k, v, u)]
+            x[i][:, t, :, 3] = bad
+            got = kda.lina_chunk_bwd(x[0], x[1], x[2], g, x[3])[:3]
+            for j, where in enumerate(clean[name]):
+                keep = [s for s in range(T) if s != t] if where is None else list(range(T))[where(t)]
+                a, b = got[j][:, keep].float(), good[j][:, keep].float()
+                # another order of the same sums: fp32 roundings, at most one bf16 step after rounding
+                lim = (2.0 ** -7 if dtype == "bf16" else 2.0 ** -17) * float(good[j].float().abs().max())
+                assert a.numel() == 0 or float((a - b).abs().max()) <= lim, (t, name, "dq dk dv".split()[j])
