@@ -28,7 +28,7 @@ struct LinaWalk {
   bool rev = false;
   int dot = kDotNone;
   float* dots = nullptr;      // [dv / 64][H][rows] fp32
-  float* snap = nullptr;      // states every kLinaGroup chunks (forward walk with kDotRow writes them)
+  float* snap = nullptr;      // states every lina_keep() chunks (forward walk with kDotRow writes them)
   float* anchor = nullptr;    // [groups][H][dv / 64][4] (reverse walk with kDotRow: <snap, state>)
   float* seg_state = nullptr; // [segments][H][dv / 64][dk * 64]
   float* seg_dec = nullptr;   // [segments][H]
@@ -45,7 +45,12 @@ struct LinaWalk {
   void* stream = nullptr;
 };
 
-constexpr int kLinaGroup = 16;  // chunks between two kept states of the backward
+constexpr int kLinaGroup = 16;  // chunks whose decay gradients one workgroup adds up
+// Chunks between two kept states of the backward (a divisor of kLinaGroup): D's error grows with the tokens
+// that it passes by differences.  Decay gradient off by, of its norm: fp32, 1,100 tokens, d = 128: 1.1e-6 at 16
+// chunks, 2.8e-7 at 4, 2.6e-7 at 1 (91, 92 and 94 us); bf16, 20 calls of 1,024 to 2,048 tokens, the worst 7.9e-7
+// at 16, 6.9e-7 at 8, 5.6e-7 at 4 (B4 H32 T8K: 1069, 1067 and 1104 us).
+constexpr int lina_keep(bool bf16) { return bf16 ? 8 : 4; }
 
 // most threads of a workgroup: walks, the decay gradient's sums, decode
 constexpr int kLinaThreads = 768, kLinaDecayThreads = 64 * kLinaGroup, kLinaDecodeThreads = 512;

@@ -17,7 +17,7 @@
 //   e_t = sum over the chunk of M_tj - M_jt, M_ij = r_ij (q_i . k_j)(u_i . v_j), i > j
 //   dg_t = sum_{i >= t} e_i + sum_{j < t} b_j - sum_{i < t} a_i + D,  D = <S, R> e^{g} at the
 //   chunk's first token; D moves from chunk to chunk by sum b - sum a, and every
-//   kLinaGroup chunks it is taken afresh from the two states, so that no rounding error
+//   lina_keep() chunks it is taken afresh from the two states, so that no rounding error
 //   travels further than that.
 //
 // Four waves walk one chain (sequence or segment, head, 64 value columns) or keep its state beside
@@ -33,7 +33,7 @@
 // work).  Rounded to bf16 (off by at most 2^-8 relative, as the output itself is) are P = r o QK^T
 // and the state where it is multiplied by q.  In the walks that a and b are taken from, the state
 // meets its rows as three terms too: D is a small difference of long sums of a and b, and with
-// two-term operands its error was 1e-5 of the gradient's norm, now 6e-7.
+// two-term operands its error was 1e-5 of the gradient's norm, with three at most 7e-7.
 #include <algorithm>
 #include <type_traits>
 
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       if constexpr (DOT == kDotRow) {
         xd = rd;
         if (it + 1 < steps) fetch(it + 1);
-        if (!REV && c % kLinaGroup == 0) store_snap<DK>(p, ch, c, tid, S);
+        if (!REV && c % lina_keep(true) == 0) store_snap<DK>(p, ch, c, tid, S);
       }
       f32x4_t acc[4];
       from_state<T, DK, DOT == kDotRow>(S, tQ(it), lane, acc);
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       store_out<T, REV>(acc, w, ch, c, wave, lane);
       add_chunk<T, DK>(S, fv, tK(it), dc, lane);
       if constexpr (DOT == kDotRow && REV)
-        if (c % kLinaGroup == 0) store_anchor<DK>(p, ch, c, tid, S);
+        if (c % lina_keep(true) == 0) store_anchor<DK>(p, ch, c, tid, S);
       lds_barrier();
     }
     store_state<DK, REV>(p, ch, tid, S);
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(3 * NT) void lina_reverse_kernel(const RevParams p)
       store_out<T, true, true>(acc, wp.w, ch, c, wave, lane);
       add_chunk<T, D, true>(S, fv, tile(it, tk), dc, lane);
       if constexpr (EXACT)
-        if (c % kLinaGroup == 0) store_anchor<D>(wp, ch, c, tid, S);
+        if (c % lina_keep(true) == 0) store_anchor<D>(wp, ch, c, tid, S);
       lds_barrier();
     }
     store_state<D, true>(wp, ch, tid, S);
@@ -483,7 +483,7 @@ __device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned bloc
       continue;
     }
     if constexpr (DOT == kDotRow && !REV)
-      if (c % kLinaGroup == 0) store_snap<DK>(p, ch, c, tid, S);
+      if (c % lina_keep(false) == 0) store_snap<DK>(p, ch, c, tid, S);
     make_p<T, DK, DOT>(sQ, sK, sV, sX, sP, dc, sdot[wave], sdot2, wave, lane);
     f32x4_t acc[4];
     from_state<T, DK, false>(S, sQ, lane, acc);
@@ -497,7 +497,7 @@ __device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned bloc
     store_out<T, REV>(acc, w, ch, c, wave, lane);
     add_chunk<T, DK>(S, fv, sK, dc, lane);
     if constexpr (DOT == kDotRow && REV)
-      if (c % kLinaGroup == 0) store_anchor<DK>(p, ch, c, tid, S);
+      if (c % lina_keep(false) == 0) store_anchor<DK>(p, ch, c, tid, S);
   }
   store_state<DK, REV>(p, ch, tid, S);
 }
@@ -786,14 +786,14 @@ __global__ __launch_bounds__(256) void lina_headsum_kernel(const float* __restri
 __global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const int* __restrict__ cs, int nseq, int T, int H,
                                                            int64_t rows, const float* __restrict__ a,
                                                            const float* __restrict__ b, const float* __restrict__ e,
-                                                           int na, int ne, const float* __restrict__ anchor,
+                                                           int na, int ne, const float* __restrict__ anchor, int keep,
                                                            const float* __restrict__ g, bool g_fixed,
                                                            float* __restrict__ dg, double* __restrict__ part) {
   __shared__ double chunk_sum[kLinaGroup];
   const int64_t grp = blockIdx.x;
   const int h = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int per = C * kLinaGroup;
-  int64_t lo, hi;
+  int64_t lo, hi, kept;  // kept: the sequence's first kept state
   int gi;
   if (cs) {
     int x = 0, y = nseq;
@@ -804,11 +804,13 @@ __global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const in
     lo = cs[x];
     hi = cs[x + 1];
     gi = (int)(grp - (lo / per + x));
+    kept = lo / (C * keep) + x;
   } else {
     const int groups = max(1, (T + per - 1) / per);
     lo = grp / groups * T;
     hi = lo + T;
     gi = (int)(grp % groups);
+    kept = grp / groups * ((T + C * keep - 1) / (C * keep));
   }
   const int64_t t = lo + (int64_t)gi * per + wave * C + lane;
   const bool in = t < hi;
@@ -831,8 +833,10 @@ __global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const in
   __syncthreads();
   double D = 0.;
   if (in) {
-    for (int x = 0; x < 4 * na; ++x) D += anchor[((size_t)grp * H + h) * 4 * na + x];
-    for (int x = 0; x < wave; ++x) D += chunk_sum[x];
+    const int from = wave / keep * keep;  // the last chunk with a kept state
+    const int64_t at = kept + (gi * kLinaGroup + from) / keep;
+    for (int x = 0; x < 4 * na; ++x) D += anchor[((size_t)at * H + h) * 4 * na + x];
+    for (int x = from; x < wave; ++x) D += chunk_sum[x];
   }
   double r = in ? ev + (pre - (bv - av)) + D : 0.;
   if (in && (g_fixed ? g[h] : g[(size_t)t * H + h]) < kLeast) r = 0.;  // a reset passes nothing on
@@ -949,8 +953,8 @@ hipError_t launch_lina_ddecay(const LinaWalk& w, const float* a, const float* b,
   const int64_t groups = w.cs ? lina_pieces(w.T, w.n, kLinaGroup) : (int64_t)w.n * (((int64_t)w.T + per - 1) / per);
   if (rows > 0 && groups > 0) {
     hipLaunchKernelGGL(lina_ddecay_kernel, dim3((unsigned)groups, (unsigned)w.H), dim3(kLinaDecayThreads), 0,
-                       (hipStream_t)w.stream, w.cs, w.n, w.T, w.H, rows, a, b, e, na, ne, anchor, w.g, w.g_fixed, dg,
-                       part);
+                       (hipStream_t)w.stream, w.cs, w.n, w.T, w.H, rows, a, b, e, na, ne, anchor, lina_keep(w.bf16),
+                       w.g, w.g_fixed, dg, part);
     const hipError_t er = hipGetLastError();
     if (er != hipSuccess) return er;
   }

@@ -180,7 +180,7 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
 // and per-token parts of the decay gradient, the per-head gradients of shared q and k.
 struct BwdLayout {
   Plan plan;
-  int64_t groups;
+  int64_t groups, kept;
   size_t off_dec, off_seg2, off_dec2, off_seg3, off_dec3, off_cs, off_list, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
 };
 
@@ -191,6 +191,8 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   const size_t seg = l.plan.split ? (size_t)l.plan.nseg : 0, state = (size_t)s.H * s.dk * s.dv * 4;
   const int64_t per = 64 * kda::kLinaGroup;
   l.groups = n_seqs >= 0 ? kda::lina_pieces(s.T, n, kda::kLinaGroup) : n * ((s.T + per - 1) / per);
+  const int64_t keep = kda::lina_keep(s.dtype == KDA_BF16);
+  l.kept = n_seqs >= 0 ? kda::lina_pieces(s.T, n, keep) : n * ((s.T + 64 * keep - 1) / (64 * keep));
   l.off_dec = up(seg * state);
   l.off_seg2 = up(l.off_dec + seg * s.H * 4);
   l.off_dec2 = up(l.off_seg2 + seg * state);
@@ -199,8 +201,8 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   l.off_cs = up(l.off_dec3 + seg * s.H * 4);
   l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 2) * 4 : 0));
   l.off_snap = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
-  l.off_anchor = up(l.off_snap + l.groups * state);
-  l.off_a = up(l.off_anchor + (size_t)l.groups * s.H * (s.dk / 64) * 4 * 4);
+  l.off_anchor = up(l.off_snap + l.kept * state);
+  l.off_a = up(l.off_anchor + (size_t)l.kept * s.H * (s.dk / 64) * 4 * 4);
   const size_t dots = (size_t)toks * s.H * 4;
   l.off_b = up(l.off_a + dots * (s.dk / 64));
   l.off_e = up(l.off_b + dots * (s.dk / 64));

@@ -346,10 +346,10 @@ struct Chain {
   __device__ __forceinline__ size_t at(const WalkParams& p, int64_t piece) const {
     return ((size_t)piece * p.w.H + h) * p.nv + vt;
   }
-  // group of kLinaGroup chunks that starts with chunk c
-  __device__ __forceinline__ int64_t group(const WalkParams& p, int c) const {
-    return p.w.cs ? lo / (C * kLinaGroup) + sq + c / kLinaGroup
-                  : (int64_t)sq * ((nch + kLinaGroup - 1) / kLinaGroup) + c / kLinaGroup;
+  // kept state at the start of chunk c
+  __device__ __forceinline__ int64_t kept(const WalkParams& p, int c) const {
+    const int keep = lina_keep(p.w.bf16);
+    return p.w.cs ? lo / (C * keep) + sq + c / keep : (int64_t)sq * ((nch + keep - 1) / keep) + c / keep;
   }
   __device__ __forceinline__ uint32_t rows(int c) const {  // tokens of chunk c
     return (uint32_t)min((int64_t)C, hi - lo - (int64_t)c * C);
@@ -714,7 +714,7 @@ template <int DK>
 __device__ __forceinline__ void store_anchor(const WalkParams& p, const Chain& ch, int c, int tid,
                                              const f32x4_t (&S)[DK / 16]) {
   const LinaWalk& w = p.w;
-  const size_t slot = ch.at(p, ch.group(p, c));
+  const size_t slot = ch.at(p, ch.kept(p, c));
   const f32x4_t* from = (const f32x4_t*)(w.snap + slot * (DK * VT));
   float d = 0.f;
 #pragma unroll
@@ -731,7 +731,7 @@ __device__ __forceinline__ void store_anchor(const WalkParams& p, const Chain& c
 template <int DK>
 __device__ __forceinline__ void store_snap(const WalkParams& p, const Chain& ch, int c, int tid,
                                            const f32x4_t (&S)[DK / 16]) {
-  f32x4_t* to = (f32x4_t*)(p.w.snap + ch.at(p, ch.group(p, c)) * (DK * VT));
+  f32x4_t* to = (f32x4_t*)(p.w.snap + ch.at(p, ch.kept(p, c)) * (DK * VT));
 #pragma unroll
   for (int ct = 0; ct < DK / 16; ++ct) to[ct * NT + tid] = S[ct];
 }

@@ -12,7 +12,7 @@ import sys
 
 import pytest
 
-from test_gpu_lina import _check_bwd, _dev, _inputs
+from test_gpu_lina import _check_bwd, _dev, _inputs, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -25,6 +25,23 @@ ROOT = os.path.dirname(HERE)
 def test_second_and_third_group(T, decay, dtype):
     """Two value tiles; dk and dv in one kernel for bf16."""
     _check_bwd(1, T, 1, 1, 128, 128, dtype, decay, seed=T)
+
+
+@pytest.mark.parametrize("B,T,Hk,H,dk,dv", [(1, 1100, 4, 4, 128, 128), (2, 1001, 4, 4, 64, 64), (1, 2100, 2, 4, 64, 128)])
+def test_fp32_decay_gradient_like_the_others(B, T, Hk, H, dk, dv):
+    """With fp32 inputs the decay gradient is held to the norm bound of every other fp32 result, 2^-20."""
+    import numpy as np
+    import torch
+
+    import gated_delta_rule_78_amd as kda
+    import lina_ref as ref
+    q, k, v, _, u = _inputs(B, T, Hk, H, dk, dv, "f32", seed=5)
+    # memories of one to some hundred tokens
+    noise = torch.randn(B, T, H, generator=torch.Generator().manual_seed(1))
+    g = -torch.logspace(-2.5, 0, H) * torch.nn.functional.softplus(noise)
+    dg = _np(kda.lina_chunk_bwd(*_dev(q, k, v, g, u))[3])
+    want = ref.lina_bwd(*(_np(x) for x in (q, k, v, g, u)))[3]
+    assert np.linalg.norm(dg - want) <= 2.0 ** -20 * np.linalg.norm(want)
 
 
 # two sequences of more than 1,024 tokens that start off a multiple of 1,024, with an empty one between
