@@ -839,7 +839,8 @@ __global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const in
     for (int x = from; x < wave; ++x) D += chunk_sum[x];
   }
   double r = in ? ev + (pre - (bv - av)) + D : 0.;
-  if (in && (g_fixed ? g[h] : g[(size_t)t * H + h]) < kLeast) r = 0.;  // a reset passes nothing on
+  // e^g under 2^-126 is zero to the walks: such a token passes nothing on, and r is what rounding left of sums
+  if (in && (g_fixed ? g[h] : g[(size_t)t * H + h]) * 1.4426950408889634 < -126.) r = 0.;
   if (dg) {
     if (in) dg[(size_t)t * H + h] = (float)r;
   } else {  // one decay for each head: the group's sum

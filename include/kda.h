@@ -471,7 +471,7 @@ int kda_lina_chunk_fwd_varlen(const kda_shape* shape, int qk_heads, const int* c
  *   dq, dk, dv          : outputs in the layout and dtype of q, k, v (sums are fp32 and rounded
  *                         once; q / k heads that serve several heads get the sum over them)
  *   d_log_decay         : fp32, layout of log_decay ([H]: summed over batch and tokens), or
- *                         NULL when not wanted.  At g = -inf it is 0, as e^g is.
+ *                         NULL when not wanted.  0 where e^g is under 2^-126, -inf among them.
  *   d_initial_state     : fp32, or NULL when not wanted
  *   workspace           : the size below, 256-byte aligned
  * Token rows after the last offset of a packed batch are not written.  No output may overlap

@@ -44,6 +44,22 @@ def test_fp32_decay_gradient_like_the_others(B, T, Hk, H, dk, dv):
     assert np.linalg.norm(dg - want) <= 2.0 ** -20 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_decay_gradient_of_decays_under_fp32(dk, dv, dtype):
+    """e^g under 2^-126, fp32's least normal number, is zero to the walks: its gradient is exactly zero, from -inf up to
+    ln 2^-126 = -87.34."""
+    import torch
+    T, H = 330, 2
+    u = torch.rand(1, T, H, generator=torch.Generator().manual_seed(7))
+    g = -0.02 * u
+    for i, deep in enumerate((-88.0, -110.0, -360.0, -450.0, -1e30, -float("inf"))):
+        g[(u >= 0.02 * i) & (u < 0.02 * (i + 1))] = deep
+    out = _check_bwd(1, T, 1, H, dk, dv, dtype, seed=61, g=g)
+    dg = out[3].cpu()
+    assert bool((dg[g < -87.5] == 0).all()) and bool((dg[g > -1] != 0).all())
+
+
 # two sequences of more than 1,024 tokens that start off a multiple of 1,024, with an empty one between
 CU = [0, 100, 1300, 1300, 2450, 2460]
 
