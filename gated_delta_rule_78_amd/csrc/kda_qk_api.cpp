@@ -13,7 +13,7 @@ int check_qk(const kda_qk_shape* s, int* es) {
   if (s->dtype != KDA_BF16 && s->dtype != KDA_F32) return KDA_ERR_DTYPE;
   if (s->tokens < 0 || s->q_heads < 1 || s->k_heads < 0 || s->d < 1) return KDA_ERR_SHAPE;
   if (s->q_heads > 65535 || s->k_heads > 65535 || s->tokens >= (int64_t(1) << 28))
-    return KDA_ERR_SHAPE;  // a launch counts its threads, up to 16 a token, in 32 bits
+    return KDA_ERR_SHAPE;
   if (!supported_width(s->d)) return KDA_ERR_UNSUPPORTED;
   if (s->norm < KDA_NORM_NONE || s->norm > KDA_NORM_L2) return KDA_ERR_UNSUPPORTED;
   if (!(s->eps >= 0.f)) return KDA_ERR_SHAPE;
@@ -61,6 +61,8 @@ int run(const kda_qk_shape* shape, const QkPtrs& p, bool bwd, void* stream) {
   int rc = check_qk(shape, &es);
   if (rc) return rc;
   const kda_qk_shape& s = *shape;
+  // the forward's blocks hold 2048 / d tokens each, the last one whole: a launch counts 2^32 - 1 threads at most
+  if (!bwd && (s.tokens + 2048 / s.d - 1) / (2048 / s.d) * 256 > 0xFFFFFFFFll) return KDA_ERR_SHAPE;
   const int64_t qd = (int64_t)s.q_heads * s.d, kd = (int64_t)s.k_heads * s.d;
   const int64_t qs = s.q_stride ? s.q_stride : qd, ks = s.k_stride ? s.k_stride : kd;
   const bool any = s.tokens > 0, keys = s.k_heads > 0;

@@ -530,7 +530,7 @@ int kda_lina_decode_tokens(const kda_shape* shape, int qk_heads, const void* q, 
 typedef enum { KDA_NORM_NONE = 0, KDA_NORM_RMS = 1, KDA_NORM_L2 = 2 } kda_norm;
 
 typedef struct {
-    long long tokens;   /* B * T, 0 <= tokens < 2^28 */
+    long long tokens;   /* B * T, 0 <= tokens < 2^28 (forward with d = 128: at most 2^28 - 16) */
     int q_heads, k_heads;
     int d;
     long long q_stride, k_stride;

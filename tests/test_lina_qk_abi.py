@@ -183,6 +183,19 @@ def test_qk_refusals(L, bwd):
         assert f(dwq=_p(11)) == ALIAS and f(ws=_p(8)) == ALIAS
 
 
+def test_qk_refuses_more_threads_than_a_launch_counts(L):
+    """Forward, d = 128: 16 tokens to a block of 256 threads, so 2^28 - 15 tokens are 2^32 threads, refused like 2^28
+    (the backward's blocks go through the tokens in strides: it takes every count under 2^28)."""
+    far = lambda i: ctypes.c_void_p(i << 42)  # tensors of 2^36 bytes, none over another
+    a = dict(Hq=1, Hk=0, d=128, rot=0, q=far(1), k=NUL, wq=NUL, wk=NUL, inv=NUL, pos=NUL, oq=far(2), ok=NUL)
+    for tokens in ((1 << 28) - 15, (1 << 28) - 1, 1 << 28):
+        assert _qk(L, tokens=tokens, **a) == SHAPE, tokens
+    # not refused for its size: at 2^28 - 16 the missing output comes first
+    assert _qk(L, tokens=(1 << 28) - 16, **dict(a, oq=NUL)) == NULL
+    assert _qk(L, tokens=(1 << 28) - 1, **dict(a, d=64, oq=NUL)) == NULL
+    assert _qk(L, True, tokens=(1 << 28) - 1, dyq=far(3), dyk=NUL, dwq=NUL, dwk=NUL, **dict(a, oq=NUL)) == NULL
+
+
 def test_binding_refuses():
     torch = pytest.importorskip("torch")
     z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt)
