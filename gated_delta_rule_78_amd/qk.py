@@ -66,7 +66,7 @@ def _shape(q, k, norm, eps, weight_offset, freqs, positions, sections, interleav
             raise ValueError("shapes: q [..., Hq, d]; k [..., Hk, d]")
     n = lead[0] if len(lead) == 1 else lead[0] * lead[1]
     s = _kda.QkShape(tokens=n, q_heads=Hq, k_heads=0 if k is None else k[0][-2], d=d, norm=_NORMS[norm],
-                     eps=float(eps), weight_offset=float(weight_offset), interleaved=int(bool(interleaved)),
+                     eps=eps, weight_offset=weight_offset, interleaved=int(interleaved),
                      dtype=_kda._dtype_code_of(dtype))
     s.q_stride = _step(qs, qt, "q")
     s.k_stride = 0 if k is None else _step(k[0], k[1], "k")
@@ -78,7 +78,7 @@ def _shape(q, k, norm, eps, weight_offset, freqs, positions, sections, interleav
         if positions[1] not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64")
         half = freqs[0][0]
-        sec = [half] if sections is None else [int(x) for x in sections]
+        sec = [half] if sections is None else sections
         if not 1 <= len(sec) <= 4 or min(sec) < 0 or sum(sec) != half:
             raise ValueError("sections: up to four counts of frequencies that add up to inv_freq's")
         want = lead if sections is None else (len(sec), *lead)
@@ -99,10 +99,11 @@ def _call(q, k, norm, eps, weight_offset, inv_freq, positions, sections, interle
         if x is not None and (not x.is_cuda or x.device != dev):
             raise ValueError(f"{nm} must be on {dev}")
     _kda._check((inv_freq, positions), ("inv_freq", "positions"), dev)
-    s, need = _shape((q.shape, q.stride(), q.dtype), None if k is None else (k.shape, k.stride(), k.dtype), norm, eps,
-                     weight_offset, None if inv_freq is None else (inv_freq.shape, inv_freq.dtype),
+    # numbers, not the objects that hold them: a tensor would be found again by its identity
+    s, need = _shape((q.shape, q.stride(), q.dtype), None if k is None else (k.shape, k.stride(), k.dtype), norm,
+                     float(eps), float(weight_offset), None if inv_freq is None else (inv_freq.shape, inv_freq.dtype),
                      None if positions is None else (positions.shape, positions.dtype),
-                     None if sections is None else tuple(sections), bool(interleaved))
+                     None if sections is None else tuple(map(int, sections)), bool(interleaved))
     return s, need, dev
 
 

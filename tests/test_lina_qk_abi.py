@@ -234,6 +234,32 @@ def test_binding_refuses():
     assert inv.dtype == torch.float64 and inv[0] == 1.0 and abs(float(inv[-1]) - 10000.0 ** (-62 / 64)) < 1e-16
 
 
+def test_qk_scalars_are_taken_by_value(L, monkeypatch):
+    """Sizes are checked once for each set of them; eps, weight_offset and sections may be tensors or arrays, whose
+    values count, not which object holds them."""
+    torch = pytest.importorskip("torch")
+    from gated_delta_rule_78_amd import qk
+
+    class OnDevice:  # what the binding looks at before a launch
+        shape, dtype, device, is_cuda = torch.Size((1, 3, 2, 64)), torch.float32, torch.device("cpu"), True
+
+        def stride(self):
+            return (384, 128, 64, 1)
+
+    monkeypatch.setattr(kda, "_check", lambda *a: None)
+    inv = kda.rope_inv_freq(64, device="cpu")
+    pos = torch.zeros(2, 1, 3, dtype=torch.int32)
+    eps, off, sec = torch.tensor(1e-6), torch.tensor(0.0), torch.tensor([16, 16])
+    for e, o, n in ((1e-6, 0.0, 16), (0.5, 1.0, 8), (0.25, 2.0, 24)):
+        eps.fill_(e)
+        off.fill_(o)
+        sec[0], sec[1] = n, 32 - n
+        s = qk._call(OnDevice(), None, "rms", eps, off, inv, pos, sec, False)[0]
+        assert abs(s.eps - e) < 1e-7 and s.weight_offset == o and list(s.sections) == [n, 32 - n, 0, 0]
+        s = qk._call(OnDevice(), None, "rms", eps, off, None, None, None, False)[0]
+        assert abs(s.eps - e) < 1e-7 and s.weight_offset == o
+
+
 @pytest.mark.parametrize("seed", [0, 1])
 def test_lina_reference_gradient_against_differences(seed):
     """The reference's gradients against central differences of its own loss, in fp64: with a
