@@ -46,10 +46,16 @@ int segment_override() {
   return v;
 }
 
-// A chain (sequence, head, 64 value columns) is walked in order; with fewer chains than compute
+// A chain (sequence, head, 64 value columns) is walked in order; with too few chains for the 256 compute
 // units it is cut into segments of L chunks, whose start states cost one more read of k and v
-// (the segments' end states first, then every segment from its own start).  Measured, bf16,
-// d = 128, forward: with 256 chains or more whole chains win; below, one segment per compute
+// (the segments' end states first, then every segment from its own start).  Measured, us, cut and
+// whole, bf16, d = 128, T = 8,192:
+//   chains     96         112        128        144        158        176          192          240
+//   forward    208, 255   204, 249   210, 239   251, 252   279, 241   347, 267     338, 253     458, 294
+//   backward   603, 950   678, 959   715, 953   849, 978   903, 959   1198, 1001   1134, 987    1404, 1030
+// (T = 32,768 with 144: 955, 980 and 3249, 3868; with 158: 1059, 939 and 3503, 3766; fp32, d = 64, T = 2,048, with
+// 158: 221, 220 and 680, 840; with 192: 304, 221 and 880, 842), so that a forward cuts up to 144 chains and a
+// backward up to 160.  Where chains are cut, one segment per compute
 // unit (work / 256: 512 chunks of 8 chains 74 us at L = 16, 87 at 8, 90 at 24), or two where
 // segments stay long, for the sake of the first pass (128 chunks of 64 chains 115 us at L = 16,
 // 116 at 32, 234 whole; 2,048 of 32 chains 860 at 128, 889 at 256, 3,620 whole).  Short segments
@@ -63,14 +69,14 @@ int segment_override() {
 // which saves the first pass and its launch: bf16, 8 heads, d = 128: 3 chunks 10.3 us against
 // 12.9, 8 chunks 16.8 and 17.4, 10 chunks 19.1 and 17.6; fp32, whose steps are dearer, 4 heads,
 // d = 64: 3 chunks 16.0 and 17.2, 4 chunks 18.8 and 17.7.
-Plan lina_plan(const kda_shape& s, int n_seqs, int nv) {
+Plan lina_plan(const kda_shape& s, int n_seqs, int nv, int most) {
   const bool packed = n_seqs >= 0;
   const int64_t nch = std::max<int64_t>(1, ((int64_t)s.T + 63) / 64);
   const int64_t n = packed ? n_seqs : s.B;
   const int64_t chains = std::max<int64_t>(1, n * s.H * nv);
   const int64_t work = (packed ? nch + n : nch * n) * s.H * nv;  // chunk steps in all
   int64_t L = nch;
-  if (packed || chains < 256) {
+  if (packed || chains <= most) {
     L = (work + 255) / 256;
     if (chains >= 256 || L >= 32) L = (work + 511) / 512;
     L = std::max<int64_t>(L, (int64_t)std::ceil(std::sqrt((double)nch * (s.dtype == KDA_BF16 ? 0.16 : 0.06))));
@@ -97,7 +103,7 @@ struct FwdLayout {
 
 FwdLayout fwd_layout(const kda_shape& s, int n_seqs) {
   FwdLayout l;
-  l.plan = lina_plan(s, n_seqs, s.dv / 64);
+  l.plan = lina_plan(s, n_seqs, s.dv / 64, 144);
   const size_t seg = l.plan.split && !l.plan.replay ? (size_t)l.plan.nseg : 0;
   l.off_dec = up(seg * s.H * s.dk * s.dv * 4);
   l.off_cs = up(l.off_dec + seg * s.H * 4);
@@ -187,7 +193,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   BwdLayout l;
   const int64_t n = n_seqs >= 0 ? n_seqs : s.B, toks = (int64_t)s.B * s.T;
-  l.plan = lina_plan(s, n_seqs, std::min(s.dk, s.dv) / 64);
+  l.plan = lina_plan(s, n_seqs, std::min(s.dk, s.dv) / 64, 160);
   const size_t seg = l.plan.split ? (size_t)l.plan.nseg : 0, state = (size_t)s.H * s.dk * s.dv * 4;
   const int64_t per = 64 * kda::kLinaGroup;
   l.groups = n_seqs >= 0 ? kda::lina_pieces(s.T, n, kda::kLinaGroup) : n * ((s.T + per - 1) / per);

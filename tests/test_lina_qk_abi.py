@@ -134,6 +134,19 @@ def test_lina_workspaces(L):
     assert _fwd(L, varlen=3, cu=_p(6), nws=v - 1) == WORKSPACE
 
 
+@pytest.mark.parametrize("B,H,d,T,fwd_cut,bwd_cut", [
+    (1, 64, 128, 8192, True, True), (1, 72, 128, 8192, True, True), (1, 79, 128, 8192, False, True),
+    (1, 88, 128, 8192, False, False), (3, 32, 128, 2048, False, False), (3, 32, 128, 512, False, False),
+    (5, 24, 128, 8192, False, False), (3, 64, 64, 4096, False, False)])
+def test_lina_chains_that_are_cut(L, B, H, d, T, fwd_cut, bwd_cut):
+    """Whole chains need no workspace forward, and the same for each sequence backward as a batch that fills the card;
+    those that are cut need their segments' states."""
+    sh = lambda n: ctypes.byref(kda.Shape(n, T, H, d, d, 64, 0))
+    assert (L.kda_lina_chunk_fwd_workspace_size(sh(B)) > 0) == fwd_cut
+    each = L.kda_lina_chunk_bwd_workspace_size(sh(16), H) // 16
+    assert (L.kda_lina_chunk_bwd_workspace_size(sh(B), H) > B * each) == bwd_cut
+
+
 def test_lina_packed_refusals(L):
     for f in (_fwd, _bwd):
         assert f(L, varlen=3, cu=None) == NULL
