@@ -28,10 +28,11 @@ struct LinaWalk {
   bool rev = false;
   int dot = kDotNone;
   float* dots = nullptr;      // [dv / 64][H][rows] fp32
-  float* snap = nullptr;      // states every lina_keep() chunks (forward walk with kDotRow writes them)
+  float* snap = nullptr;      // states every lina_keep() chunks but the first (forward walk with kDotRow writes them)
+  const float* snap0 = nullptr;  // reverse walk with kDotRow: the first, the caller's [n, H, dv, dk], or NULL for zeros
   float* anchor = nullptr;    // [groups][H][dv / 64][4] (reverse walk with kDotRow: <snap, state>)
-  float* seg_state = nullptr; // [segments][H][dv / 64][dk * 64]
-  float* seg_dec = nullptr;   // [segments][H]
+  float* seg_state = nullptr; // end states [lina_ends][H][dv / 64][dk * 64], then kept start states
+  float* seg_dec = nullptr;   // [lina_ends][H]
   // batch
   const int* cs = nullptr;    // clamped offsets of a packed batch [n + 1] and its chunks of a segment, or NULL
   const int* list = nullptr;  // its segments in the order they are dealt, [slots][2]
@@ -58,6 +59,16 @@ constexpr int kLinaThreads = 768, kLinaDecayThreads = 64 * kLinaGroup, kLinaDeco
 // Segments (or groups of `per` chunks) of a batch: sequence i starts at
 // offset / (64 per) + i, so that every sequence has at least one.
 inline int64_t lina_pieces(int64_t rows, int64_t n, int64_t per) { return rows / (64 * per) + n; }
+
+// Segments from whose end another one starts.  A packed sequence that starts at `offset` has at most
+// (its rows - 1) / (64 L) of them, from slot offset / (64 L) on, so that no sequence reaches the next
+// one's and a batch of many short ones needs none.
+inline int64_t lina_ends(bool packed, int64_t T, int64_t n, int64_t L) {
+  const int64_t nch = T > 0 ? (T + 63) / 64 : 1;
+  return packed ? T / (64 * L) : n * ((nch + L - 1) / L - 1);
+}
+// States that a cut batch keeps in all: those ends, and the start state of each cut sequence (fewer than ends).
+inline int64_t lina_seg_states(int64_t ends, int64_t n) { return ends + (ends < n ? ends : n); }
 
 // up to three walks of one call: the end states of their segments, where they are split
 hipError_t launch_lina_segments(const LinaWalk* w, int n);

@@ -176,7 +176,7 @@ __global__ __launch_bounds__(2 * NT) void lina_walk_bf16_kernel(const WalkParams
       if constexpr (DOT == kDotRow) {
         xd = rd;
         if (it + 1 < steps) fetch(it + 1);
-        if (!REV && c % lina_keep(true) == 0) store_snap<DK>(p, ch, c, tid, S);
+        if (!REV && c > 0 && c % lina_keep(true) == 0) store_snap<DK>(p, ch, c, tid, S);
       }
       f32x4_t acc[4];
       from_state<T, DK, DOT == kDotRow>(S, tQ(it), lane, acc);
@@ -483,7 +483,7 @@ __device__ __forceinline__ void walk_f32_body(const WalkParams& p, unsigned bloc
       continue;
     }
     if constexpr (DOT == kDotRow && !REV)
-      if (c % lina_keep(false) == 0) store_snap<DK>(p, ch, c, tid, S);
+      if (c > 0 && c % lina_keep(false) == 0) store_snap<DK>(p, ch, c, tid, S);
     make_p<T, DK, DOT>(sQ, sK, sV, sX, sP, dc, sdot[wave], sdot2, wave, lane);
     f32x4_t acc[4];
     from_state<T, DK, false>(S, sQ, lane, acc);
@@ -602,10 +602,10 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 3 : 1) void lina_segment_kerne
     add_chunk<T, DK>(S, fv, t, dc, lane);
     lds_barrier();
   }
-  f32x4_t* to = (f32x4_t*)(w.seg_state + ch.at(p, ch.seg) * (DK * VT));
+  f32x4_t* to = (f32x4_t*)(w.seg_state + ch.at(p, ch.end(rev, ch.sg)) * (DK * VT));
 #pragma unroll
   for (int ct = 0; ct < DK / 16; ++ct) to[ct * NT + tid] = S[ct];
-  if (tid == 0 && ch.vt == 0) w.seg_dec[(size_t)ch.seg * w.H + ch.h] = total;
+  if (tid == 0 && ch.vt == 0) w.seg_dec[(size_t)ch.end(rev, ch.sg) * w.H + ch.h] = total;
 }
 
 template <typename K, typename P>
@@ -673,6 +673,7 @@ WalkParams walk_params(const LinaWalk& w) {
   p.rows = w.cs ? w.T : (int64_t)w.n * w.T;
   const int64_t nch = ((int64_t)w.T + C - 1) / C;
   p.nseg = w.cs ? lina_pieces(w.T, w.n, w.L) : (int64_t)w.n * (nch > 0 ? (nch + w.L - 1) / w.L : 1);
+  p.ends = lina_ends(w.cs != nullptr, w.T, w.n, w.L);
   return p;
 }
 
@@ -793,7 +794,7 @@ __global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const in
   const int64_t grp = blockIdx.x;
   const int h = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int per = C * kLinaGroup;
-  int64_t lo, hi, kept;  // kept: the sequence's first kept state
+  int64_t lo, hi, kept;  // kept: the sequence's first anchor
   int gi;
   if (cs) {
     int x = 0, y = nseq;
@@ -833,7 +834,7 @@ __global__ __launch_bounds__(kLinaDecayThreads) void lina_ddecay_kernel(const in
   __syncthreads();
   double D = 0.;
   if (in) {
-    const int from = wave / keep * keep;  // the last chunk with a kept state
+    const int from = wave / keep * keep;  // the last chunk with an anchor
     const int64_t at = kept + (gi * kLinaGroup + from) / keep;
     for (int x = 0; x < 4 * na; ++x) D += anchor[((size_t)at * H + h) * 4 * na + x];
     for (int x = from; x < wave; ++x) D += chunk_sum[x];

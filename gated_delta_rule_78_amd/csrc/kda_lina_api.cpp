@@ -35,6 +35,7 @@ struct Plan {
   bool split;
   bool replay;  // the forward's segments make their start states themselves
   int64_t nseg;
+  int64_t ends, states;  // end states of segments; with the kept start states
 };
 
 // KDA_LINA_SEGMENT=n pins the chunks of a segment (tuning aid, and the tests' forced splits).
@@ -88,6 +89,8 @@ Plan lina_plan(const kda_shape& s, int n_seqs, int nv, int most) {
   p.split = L < nch;
   p.replay = p.split && nch <= (s.dtype == KDA_BF16 ? 8 : 3);
   p.nseg = packed ? kda::lina_pieces(s.T, n, L) : n * ((nch + L - 1) / L);
+  p.ends = p.split ? kda::lina_ends(packed, s.T, n, L) : 0;
+  p.states = kda::lina_seg_states(p.ends, n);
   return p;
 }
 
@@ -104,9 +107,9 @@ struct FwdLayout {
 FwdLayout fwd_layout(const kda_shape& s, int n_seqs) {
   FwdLayout l;
   l.plan = lina_plan(s, n_seqs, s.dv / 64, 144);
-  const size_t seg = l.plan.split && !l.plan.replay ? (size_t)l.plan.nseg : 0;
-  l.off_dec = up(seg * s.H * s.dk * s.dv * 4);
-  l.off_cs = up(l.off_dec + seg * s.H * 4);
+  const size_t some = l.plan.replay ? 0 : 1;
+  l.off_dec = up(some * l.plan.states * s.H * s.dk * s.dv * 4);
+  l.off_cs = up(l.off_dec + some * l.plan.ends * s.H * 4);
   l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 2) * 4 : 0));
   l.bytes = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
   return l;
@@ -186,7 +189,7 @@ int fwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const vo
 // and per-token parts of the decay gradient, the per-head gradients of shared q and k.
 struct BwdLayout {
   Plan plan;
-  int64_t groups, kept;
+  int64_t groups;
   size_t off_dec, off_seg2, off_dec2, off_seg3, off_dec3, off_cs, off_list, off_snap, off_anchor, off_a, off_b, off_e, off_part, off_share, bytes;
 };
 
@@ -194,21 +197,22 @@ BwdLayout bwd_layout(const kda_shape& s, int Hk, int n_seqs) {
   BwdLayout l;
   const int64_t n = n_seqs >= 0 ? n_seqs : s.B, toks = (int64_t)s.B * s.T;
   l.plan = lina_plan(s, n_seqs, std::min(s.dk, s.dv) / 64, 160);
-  const size_t seg = l.plan.split ? (size_t)l.plan.nseg : 0, state = (size_t)s.H * s.dk * s.dv * 4;
+  const size_t seg = (size_t)l.plan.states, ends = (size_t)l.plan.ends, state = (size_t)s.H * s.dk * s.dv * 4;
   const int64_t per = 64 * kda::kLinaGroup;
   l.groups = n_seqs >= 0 ? kda::lina_pieces(s.T, n, kda::kLinaGroup) : n * ((s.T + per - 1) / per);
   const int64_t keep = kda::lina_keep(s.dtype == KDA_BF16);
-  l.kept = n_seqs >= 0 ? kda::lina_pieces(s.T, n, keep) : n * ((s.T + 64 * keep - 1) / (64 * keep));
+  const int64_t anchors = n_seqs >= 0 ? kda::lina_pieces(s.T, n, keep) : n * ((s.T + 64 * keep - 1) / (64 * keep));
+  const int64_t kept = kda::lina_ends(n_seqs >= 0, s.T, n, keep);  // the start of a sequence is the caller's
   l.off_dec = up(seg * state);
-  l.off_seg2 = up(l.off_dec + seg * s.H * 4);
+  l.off_seg2 = up(l.off_dec + ends * s.H * 4);
   l.off_dec2 = up(l.off_seg2 + seg * state);
-  l.off_seg3 = up(l.off_dec2 + seg * s.H * 4);
+  l.off_seg3 = up(l.off_dec2 + ends * s.H * 4);
   l.off_dec3 = up(l.off_seg3 + seg * state);
-  l.off_cs = up(l.off_dec3 + seg * s.H * 4);
+  l.off_cs = up(l.off_dec3 + ends * s.H * 4);
   l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 2) * 4 : 0));
   l.off_snap = up(l.off_list + (n_seqs >= 0 ? (size_t)l.plan.nseg * 8 : 0));
-  l.off_anchor = up(l.off_snap + l.kept * state);
-  l.off_a = up(l.off_anchor + (size_t)l.kept * s.H * (s.dk / 64) * 4 * 4);
+  l.off_anchor = up(l.off_snap + kept * state);
+  l.off_a = up(l.off_anchor + (size_t)anchors * s.H * (s.dk / 64) * 4 * 4);
   const size_t dots = (size_t)toks * s.H * 4;
   l.off_b = up(l.off_a + dots * (s.dk / 64));
   l.off_e = up(l.off_b + dots * (s.dk / 64));
@@ -322,6 +326,7 @@ int bwd_impl(const kda_shape* shape, int Hk, const int* cu, int n_seqs, const Bw
   wk.rev = true;
   wk.dots = db;
   wk.anchor = anchor;
+  wk.snap0 = p.s0;
   wk.seg_state = (float*)(ws + l.off_seg2);
   wk.seg_dec = (float*)(ws + l.off_dec2);
   wv.q = k;  // and the start state's gradient

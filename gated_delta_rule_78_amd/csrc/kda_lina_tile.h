@@ -285,11 +285,13 @@ struct WalkParams {
   int nv;        // value tiles
   int64_t rows;  // tokens in all
   int64_t nseg;  // segment slots
+  int64_t ends;  // end states
 };
 
 // A workgroup's place: its segment of a sequence, its head and its 64 value columns.
 struct Chain {
-  int64_t seg, lo, hi;  // segment slot; the sequence's tokens [lo, hi)
+  int64_t lo, hi;       // the sequence's tokens [lo, hi)
+  int64_t base;         // its first end state
   int h, vt, sq;        // head, value tile, sequence
   int sg, nsg;          // segment of the sequence, its segments
   int nch;              // the sequence's chunks
@@ -308,7 +310,7 @@ struct Chain {
     const int64_t slot = block >> 3;
     const int64_t unit = slot / share * 8 + (block & 7);
     const int in = (int)(slot % share);
-    seg = unit / hk;
+    int64_t seg = unit / hk;
     if (seg >= p.nseg) return false;
     h = (int)(unit % hk) * (w.H / hk) + in / p.nv;
     vt = in % p.nv;
@@ -318,15 +320,16 @@ struct Chain {
       sg = w.list[2 * seg + 1];
       lo = w.cs[sq];
       hi = w.cs[sq + 1];
-      seg = lo / ((int64_t)C * L) + sq + sg;
+      base = lo / ((int64_t)C * L);
     } else {
       const int64_t per = p.nseg / w.n;
       sq = (int)(seg / per);
       sg = (int)(seg % per);
       lo = (int64_t)sq * w.T;
       hi = lo + w.T;
+      base = sq * (per - 1);
     }
-    seg = uniform64(seg);  // scalar from here on: buffer descriptors are made from them
+    base = uniform64(base);  // scalar from here on: buffer descriptors are made from them
     lo = uniform64(lo);
     hi = uniform64(hi);
     sq = (int)uniform64(sq);
@@ -342,14 +345,23 @@ struct Chain {
     tail = rev ? sg == 0 : sg == nsg - 1;
     return true;
   }
-  // slot of this chain in [segments or groups][H][value tiles]
+  // slot of this chain in [end states or kept states][H][value tiles]
   __device__ __forceinline__ size_t at(const WalkParams& p, int64_t piece) const {
     return ((size_t)piece * p.w.H + h) * p.nv + vt;
   }
-  // kept state at the start of chunk c
-  __device__ __forceinline__ int64_t kept(const WalkParams& p, int c) const {
+  // end state of segment s, in walk order the next one's start: all but the last have one
+  __device__ __forceinline__ int64_t end(bool rev, int s) const { return base + s - (rev ? 1 : 0); }
+  // where a cut sequence's start state is kept, after the end states
+  __device__ __forceinline__ int64_t start(const WalkParams& p) const { return p.ends + (p.ends < p.w.n ? base : sq); }
+  // anchor at the start of chunk c, a multiple of lina_keep()
+  __device__ __forceinline__ int64_t anchor(const WalkParams& p, int c) const {
     const int keep = lina_keep(p.w.bf16);
     return p.w.cs ? lo / (C * keep) + sq + c / keep : (int64_t)sq * ((nch + keep - 1) / keep) + c / keep;
+  }
+  // kept state there, c > 0: laid out as the end states are
+  __device__ __forceinline__ int64_t kept(const WalkParams& p, int c) const {
+    const int keep = lina_keep(p.w.bf16);
+    return (p.w.cs ? lo / (C * keep) : (int64_t)sq * ((nch + keep - 1) / keep - 1)) + c / keep - 1;
   }
   __device__ __forceinline__ uint32_t rows(int c) const {  // tokens of chunk c
     return (uint32_t)min((int64_t)C, hi - lo - (int64_t)c * C);
@@ -386,7 +398,7 @@ __device__ __forceinline__ void each_state(const LinaWalk& w, const Chain& ch, i
 }
 
 // The state a walk starts from: the caller's, carried over the segments before this one.  Of a chain
-// in several segments it comes from the last one's slot (keep_start), because that one may write
+// in several segments it comes from a copy (keep_start), because the last one may write
 // its final state over the caller's while others have not begun.
 template <int DK>
 __device__ __forceinline__ void start_state(const WalkParams& p, const Chain& ch, bool rev, int tid,
@@ -397,7 +409,7 @@ __device__ __forceinline__ void start_state(const WalkParams& p, const Chain& ch
   for (int ct = 0; ct < DK / 16; ++ct) S[ct] = zero4();
   if (w.s0) {
     if (kept) {
-      const f32x4_t* from = (const f32x4_t*)(w.seg_state + ch.at(p, ch.seg - ch.sg + (rev ? 0 : ch.nsg - 1)) * (DK * VT));
+      const f32x4_t* from = (const f32x4_t*)(w.seg_state + ch.at(p, ch.start(p)) * (DK * VT));
 #pragma unroll
       for (int ct = 0; ct < DK / 16; ++ct) S[ct] = from[ct * NT + tid];
     } else {
@@ -408,7 +420,7 @@ __device__ __forceinline__ void start_state(const WalkParams& p, const Chain& ch
   const int cnt = rev ? ch.nsg - 1 - ch.sg : ch.sg;
 #pragma unroll 2
   for (int j = 0; j < cnt; ++j) {
-    const int64_t s = ch.seg - ch.sg + (rev ? ch.nsg - 1 - j : j);
+    const int64_t s = ch.end(rev, rev ? ch.nsg - 1 - j : j);
     const float d = w.seg_dec[(size_t)s * w.H + ch.h];
     const f32x4_t* B = (const f32x4_t*)(w.seg_state + ch.at(p, s) * (DK * VT));
 #pragma unroll
@@ -420,12 +432,12 @@ __device__ __forceinline__ void start_state(const WalkParams& p, const Chain& ch
   }
 }
 
-// The caller's start state into the slot of the chain's last segment, from whose end nobody starts.
+// The caller's start state of a chain in several segments, copied by its last one, from whose end nobody starts.
 template <int DK>
 __device__ __forceinline__ void keep_start(const WalkParams& p, const Chain& ch, int tid) {
   const LinaWalk& w = p.w;
   if (!w.s0 || ch.nsg == 1) return;
-  f32x4_t* to = (f32x4_t*)(w.seg_state + ch.at(p, ch.seg) * (DK * VT));
+  f32x4_t* to = (f32x4_t*)(w.seg_state + ch.at(p, ch.start(p)) * (DK * VT));
   f32x4_t S[DK / 16];
   each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
 #pragma unroll
@@ -714,18 +726,25 @@ template <int DK>
 __device__ __forceinline__ void store_anchor(const WalkParams& p, const Chain& ch, int c, int tid,
                                              const f32x4_t (&S)[DK / 16]) {
   const LinaWalk& w = p.w;
-  const size_t slot = ch.at(p, ch.kept(p, c));
-  const f32x4_t* from = (const f32x4_t*)(w.snap + slot * (DK * VT));
+  const f32x4_t* from = (const f32x4_t*)(w.snap + ch.at(p, ch.kept(p, c)) * (DK * VT)) + tid;
+  int step = NT;
+  if (c == 0) {  // the caller's, its rows this walk's columns (s_t): row 16 ct + 4 g of column 16 wave + n
+    const int lane = tid & 63, vc = ch.vt * VT + 16 * (tid >> 6) + (lane & 15);
+    from = (const f32x4_t*)(w.snap0 + (((size_t)ch.sq * w.H + ch.h) * w.dv + vc) * DK) + (lane >> 4);
+    step = 4;
+  }
   float d = 0.f;
+  if (c > 0 || w.snap0) {
 #pragma unroll
-  for (int ct = 0; ct < DK / 16; ++ct) {
-    const f32x4_t x = from[ct * NT + tid];
+    for (int ct = 0; ct < DK / 16; ++ct) {
+      const f32x4_t x = from[ct * step];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d = fmaf(x[i], S[ct][i], d);
+      for (int i = 0; i < 4; ++i) d = fmaf(x[i], S[ct][i], d);
+    }
   }
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) d += __shfl_xor(d, off);
-  if ((tid & 63) == 0) w.anchor[slot * 4 + (tid >> 6)] = expf(ch.decay_log(w, ch.lo + (int64_t)c * C)) * d;
+  if ((tid & 63) == 0) w.anchor[ch.at(p, ch.anchor(p, c)) * 4 + (tid >> 6)] = expf(ch.decay_log(w, ch.lo + (int64_t)c * C)) * d;
 }
 
 template <int DK>

@@ -71,6 +71,45 @@ def test_packed_groups(dtype, dk, dv):
         assert bool((x[:, CU[-1]:] == 0).all())
 
 
+def _short_and_long(pieces, gap):
+    """Offsets of sequences of 0 to 12 tokens around longer ones of `pieces` tokens."""
+    cu = [0]
+    for p in pieces:
+        for i in range(gap):
+            cu.append(cu[-1] + (5 * i) % 13)
+        cu.append(cu[-1] + p)
+    return cu
+
+
+# more sequences than end states, and the reverse; both sequences over 1,000 tokens are cut
+@pytest.mark.parametrize("gap", [20, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cut_sequences_among_many(dtype, gap):
+    """Start and end states of cut sequences have room of their own, whatever lies between them; the state in
+    place gives the same."""
+    import torch
+
+    import gated_delta_rule_78_amd as kda
+    import lina_ref as ref
+    from test_gpu_lina import _out, _state
+    import numpy as np
+    cu, H = _short_and_long((1200, 700, 1101), gap), 2
+    T, n = cu[-1] + 3, len(cu) - 1
+    _check_bwd(1, T, 1, H, 64, 64, dtype, cu=cu, seed=71)
+    q, k, v, g, _ = _inputs(1, T, 1, H, 64, 64, dtype, seed=72)
+    S0 = torch.randn(n, H, 64, 64, generator=torch.Generator().manual_seed(3))
+    qd, kd, vd, gd, s = _dev(q, k, v, g, S0)
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, sT = kda.lina_chunk_fwd(qd, kd, vd, gd, initial_state=s, cu_seqlens=cud)
+    o2, s2 = kda.lina_chunk_fwd(qd, kd, vd, gd, initial_state=s, final_state=s, cu_seqlens=cud)
+    assert s2 is s and torch.equal(o[:, :cu[-1]], o2[:, :cu[-1]]) and torch.equal(sT, s)
+    rs = ref.packed(cu, ref.lina_fwd, *(_np(x) for x in (q, k, v, g)), states=(_np(S0),))
+    ra = ref.packed(cu, ref.lina_fwd, *(np.abs(_np(x)) for x in (q, k, v)), _np(g), states=(np.abs(_np(S0)),))
+    for i, (lo, hi) in enumerate(zip(cu, cu[1:])):
+        _out(o[:, lo:hi], rs[i][0], ra[i][0], dtype, T, f"o of {i}")
+        _state(sT[i:i + 1], rs[i][1], ra[i][1], T, f"state of {i}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_whole_chains(dtype):
     """256 chains of four chunks: none is cut."""

@@ -147,6 +147,22 @@ def test_lina_chains_that_are_cut(L, B, H, d, T, fwd_cut, bwd_cut):
     assert (L.kda_lina_chunk_bwd_workspace_size(sh(B), H) > B * each) == bwd_cut
 
 
+@pytest.mark.parametrize("T,n", [(131072, 1024), (131072, 4096), (131072, 16384), (5000, 5000), (0, 4096)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_lina_packed_workspaces_do_not_grow_with_states(L, T, n, dtype):
+    """Only segments that others start from and the backward's kept states take a state's room: none of either for a short
+    sequence.  What each further sequence may take is a list entry or two and the sums of its decay gradient."""
+    H, d = 32, 128
+    state = H * d * d * 4
+    fwd = lambda n: L.kda_lina_chunk_fwd_varlen_workspace_size(ctypes.byref(kda.Shape(1, T, H, d, d, 64, dtype)), n)
+    bwd = lambda n: L.kda_lina_chunk_bwd_varlen_workspace_size(ctypes.byref(kda.Shape(1, T, H, d, d, 64, dtype)), H, n)
+    rows = 4 * T * H * (2 * (d // 64) + d // 64)  # sums per token
+    keep, least = (8, 4)[dtype], 4  # chunks between kept states; a segment's, at the least, in a batch this wide
+    ends = 2 * (T // (64 * least)) * state
+    assert 0 < fwd(n) <= ends + 64 * n + T + 4096
+    assert 0 < bwd(n) <= 3 * ends + T // (64 * keep) * state + rows + n * H * 64 + T * H + 16384
+
+
 def test_lina_packed_refusals(L):
     for f in (_fwd, _bwd):
         assert f(L, varlen=3, cu=None) == NULL
