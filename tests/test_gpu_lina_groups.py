@@ -10,9 +10,11 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 
-from test_gpu_lina import _check_bwd, _dev, _inputs, _np
+import lina_ref as ref
+from test_gpu_lina import _check_bwd, _check_fwd, _dev, _inputs, _np, _out, _state
 
 pytestmark = pytest.mark.gpu
 
@@ -30,11 +32,9 @@ def test_second_and_third_group(T, decay, dtype):
 @pytest.mark.parametrize("B,T,Hk,H,dk,dv", [(1, 1100, 4, 4, 128, 128), (2, 1001, 4, 4, 64, 64), (1, 2100, 2, 4, 64, 128)])
 def test_fp32_decay_gradient_like_the_others(B, T, Hk, H, dk, dv):
     """With fp32 inputs the decay gradient is held to the norm bound of every other fp32 result, 2^-20."""
-    import numpy as np
     import torch
 
     import gated_delta_rule_78_amd as kda
-    import lina_ref as ref
     q, k, v, _, u = _inputs(B, T, Hk, H, dk, dv, "f32", seed=5)
     # memories of one to some hundred tokens
     noise = torch.randn(B, T, H, generator=torch.Generator().manual_seed(1))
@@ -90,9 +90,6 @@ def test_cut_sequences_among_many(dtype, gap):
     import torch
 
     import gated_delta_rule_78_amd as kda
-    import lina_ref as ref
-    from test_gpu_lina import _out, _state
-    import numpy as np
     cu, H = _short_and_long((1200, 700, 1101), gap), 2
     T, n = cu[-1] + 3, len(cu) - 1
     _check_bwd(1, T, 1, H, 64, 64, dtype, cu=cu, seed=71)
@@ -114,6 +111,20 @@ def test_cut_sequences_among_many(dtype, gap):
 def test_whole_chains(dtype):
     """256 chains of four chunks: none is cut."""
     _check_bwd(2, 200, 64, 128, 64, 64, dtype, seed=17)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [100, 150])
+def test_chains_around_the_border(H, dtype):
+    """100 chains of six chunks are cut both ways, 150 backward only."""
+    _check_fwd(1, 330, H // 2, H, 64, 64, dtype, seed=H)
+    _check_bwd(1, 330, H // 2, H, 64, 64, dtype, seed=H)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_chain_of_one_head(dtype):
+    _check_fwd(1, 8200, 1, 1, 64, 64, dtype, seed=81)
+    _check_bwd(1, 8200, 1, 1, 64, 64, dtype, seed=81)
 
 
 CHILD = r"""
