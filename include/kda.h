@@ -444,11 +444,11 @@ int kda_gdn2_decode_tokens(const kda_shape* shape, const void* q, const void* k,
  *   final_state    : [B, H, dk, dv] fp32, or NULL (not written); may equal initial_state
  *   workspace      : kda_lina_chunk_fwd_workspace_size(shape) bytes, 256-byte aligned (0 bytes,
  *                    and NULL accepted, when the chains are walked whole or are very short;
- *                    with fewer chains than compute units it holds the end states of their
- *                    segments, for a packed batch its offsets and list of segments too)
+ *                    where there are few, they are cut, and it holds the end states of their
+ *                    segments; for a packed batch its offsets and list of segments too)
  * Arithmetic: fp32 sums, decays and states; with bf16 inputs the products r o q.k and the state
  * as q meets it are rounded to bf16 (as o is); what is added to the state is kept to 2^-24.
- * A non-finite v_t reaches the outputs from token t on only.  Alignment: 16 bytes for q, k, v,
+ * A non-finite v_t reaches the outputs from token t on only (an infinity as one or as NaN).  Alignment: 16 bytes for q, k, v,
  * o and the states, 4 for log_decay.  Aliasing, packed batches (cu_seqlens, n_seqs, states of
  * [n_seqs, H, dk, dv], token rows after the last offset not written) and errors as
  * kda_chunk_fwd_ws and kda_chunk_fwd_varlen.  H <= 65535; n_seqs <= 2^24; more than about
@@ -468,12 +468,18 @@ int kda_lina_chunk_fwd_varlen(const kda_shape* shape, int qk_heads, const int* c
  * Backward of kda_lina_chunk_fwd(_varlen): the gradients of
  *   L = sum_t <d_o_t, o_t> + <d_final_state, S_T> .
  *   d_o                 : [B, T, H, dv], dtype of q;  d_final_state : fp32 or NULL (zeros)
- *   dq, dk, dv          : outputs in the layout and dtype of q, k, v (sums are fp32 and rounded
- *                         once; q / k heads that serve several heads get the sum over them)
+ *   dq, dk, dv          : outputs in the layout and dtype of q, k, v (sums are fp32; q / k heads
+ *                         that serve several heads get the sum over them, rounded once).  With
+ *                         bf16 inputs the scores r o (x.y) are rounded to bf16 before their sums
+ *                         with the third operand, and so is the state as it meets its rows: for
+ *                         dv always, for dq and dk when d_log_decay is NULL.  When it is not, their
+ *                         state is kept to 2^-24, so that dq and dk differ by these roundings.
  *   d_log_decay         : fp32, layout of log_decay ([H]: summed over batch and tokens), or
  *                         NULL when not wanted.  0 where e^g is under 2^-126, -inf among them.
  *   d_initial_state     : fp32, or NULL when not wanted
  *   workspace           : the size below, 256-byte aligned
+ * A non-finite q_t, k_t, v_t or d_o_t reaches only those rows of dq, dk and dv that depend on it;
+ * d_log_decay is carried over tokens by differences and may lose others.
  * Token rows after the last offset of a packed batch are not written.  No output may overlap
  * an input, another output or the workspace (KDA_ERR_ALIAS).  Results do not depend on timing:
  * every sum has a fixed order.
