@@ -19,6 +19,7 @@ __all__ = ["chunk_fwd", "chunk_records", "chunk_apply_records", "chunk_fwd_debug
            "sfda_chunk_fwd", "sfda_decode_step", "sfda_decode_tokens", "chunk_bwd", "chunk_bwd_varlen",
            "gdn2_chunk_bwd", "bwd_workspace_size",
            "lina_chunk_fwd", "lina_chunk_bwd", "lina_decode_step", "lina_decode_tokens",
+           "gdr_chunk_fwd", "gdr_chunk_bwd", "gdr_decode_step", "gdr_decode_tokens", "verify_drafts",
            "qk_norm_rope", "qk_norm_rope_bwd", "rope_inv_freq",
            "workspace_size", "pick_path", "chunk_fwd_noalloc", "lib", "version", "status_string",
            "LIB_PATH", "KdaError", "Shape", "BF16", "F32"]
@@ -141,6 +142,30 @@ def lib() -> ctypes.CDLL:
         L.kda_lina_decode_step.restype = I
         L.kda_lina_decode_tokens.argtypes = [SP, I, P, P, P, P, I, P, P, P]
         L.kda_lina_decode_tokens.restype = I
+        L.kda_gdr_chunk_fwd_workspace_size.argtypes = [SP]
+        L.kda_gdr_chunk_fwd_workspace_size.restype = Z
+        L.kda_gdr_chunk_fwd.argtypes = [SP, I] + [P] * 9 + [Z, P]
+        L.kda_gdr_chunk_fwd.restype = I
+        L.kda_gdr_chunk_fwd_varlen_workspace_size.argtypes = [SP, I]
+        L.kda_gdr_chunk_fwd_varlen_workspace_size.restype = Z
+        L.kda_gdr_chunk_fwd_varlen.argtypes = [SP, I, P, I] + [P] * 9 + [Z, P]
+        L.kda_gdr_chunk_fwd_varlen.restype = I
+        L.kda_gdr_chunk_bwd_workspace_size.argtypes = [SP]
+        L.kda_gdr_chunk_bwd_workspace_size.restype = Z
+        L.kda_gdr_chunk_bwd.argtypes = [SP, I] + [P] * 15 + [Z, P]
+        L.kda_gdr_chunk_bwd.restype = I
+        L.kda_gdr_chunk_bwd_varlen_workspace_size.argtypes = [SP, I]
+        L.kda_gdr_chunk_bwd_varlen_workspace_size.restype = Z
+        L.kda_gdr_chunk_bwd_varlen.argtypes = [SP, I, P, I] + [P] * 15 + [Z, P]
+        L.kda_gdr_chunk_bwd_varlen.restype = I
+        L.kda_gdr_decode_step.argtypes = [SP, I] + [P] * 8
+        L.kda_gdr_decode_step.restype = I
+        L.kda_gdr_decode_tokens.argtypes = [SP, I, P, I] + [P] * 8
+        L.kda_gdr_decode_tokens.restype = I
+        L.kda_verify_drafts_workspace_size.argtypes = [I, I, I, I]
+        L.kda_verify_drafts_workspace_size.restype = Z
+        L.kda_verify_drafts.argtypes = [I, I, I, I] + [P] * 8 + [Z, P]
+        L.kda_verify_drafts.restype = I
         QP = ctypes.POINTER(QkShape)
         L.kda_qk_norm_rope.argtypes = [QP] + [P] * 9
         L.kda_qk_norm_rope.restype = I
@@ -743,4 +768,6 @@ def sfda_chunk_bwd(q, k, v, lam, beta, d_o, initial_state=None, d_final_state=No
 
 
 from .lina import lina_chunk_bwd, lina_chunk_fwd, lina_decode_step, lina_decode_tokens  # noqa: E402
+from .gdr import gdr_chunk_bwd, gdr_chunk_fwd, gdr_decode_step, gdr_decode_tokens  # noqa: E402
+from .verify import verify_drafts  # noqa: E402
 from .qk import qk_norm_rope, qk_norm_rope_bwd, rope_inv_freq  # noqa: E402

@@ -22,7 +22,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_state.hip", "kda_varlen.hip", "kda_records.hip", "kda_walk.hip", "kda_bwd.hip",
-           "kda_noalloc.hip", "kda_lina_api.cpp", "kda_lina.hip", "kda_lina_decode.hip", "kda_qk_api.cpp", "kda_qk.hip"]
+           "kda_noalloc.hip", "kda_lina_api.cpp", "kda_lina.hip", "kda_lina_decode.hip", "kda_qk_api.cpp", "kda_qk.hip",
+           "kda_gdr_api.cpp", "kda_gdr.hip", "kda_gdr_bwd.hip", "kda_gdr_decode.hip", "kda_verify_api.cpp", "kda_verify.hip"]
 
 
 def _compile(src: str, verbose: bool) -> str:

@@ -690,8 +690,8 @@ WalkParams walk_params(const LinaWalk& w) {
 // (1.7 shares): 308 us whole, 273 cut; 0.6 of all (2.2 shares): 369 and 283; 24 like ones: 218 whole.
 constexpr int NTB = 1024;
 __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T, int least,
-                                                           int chains, int64_t slots, int* __restrict__ cs,
-                                                           int* __restrict__ list) {
+                                                           int chains, int cut, int64_t slots,
+                                                           int* __restrict__ cs, int* __restrict__ list) {
   __shared__ int part[NTB / 64], from[64], total, longest, used;
   const int tid = threadIdx.x, lane = tid & 63, per = (nseq + NTB - 1) / NTB;
   const int s0 = min(nseq, tid * per), s1 = min(nseq, s0 + per);
@@ -728,7 +728,7 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
     atomicMax(&longest, top);
   }
   __syncthreads();
-  L = (int64_t)longest * 160 > (int64_t)total * chains ? least : max(least, longest);  // 1.6 shares of 256
+  L = (int64_t)longest * cut > (int64_t)total * chains ? least : max(least, longest);  // cut 160: 1.6 shares of 256
   if (tid == 0) cs[nseq + 1] = L;
   auto cls = [&](int len) { return 63 - (int)((int64_t)len * 63 / L); };
   each([&](int i, int end, int nch, int nsg) {
@@ -930,8 +930,9 @@ hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv) {
   return want ? reverse<64, true>(p) : reverse<64, false>(p);
 }
 
-hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int chains, int* cs, int* list, void* stream) {
-  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, L, chains,
+hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int chains, int* cs, int* list, void* stream,
+                               int cut) {
+  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, L, chains, cut,
                      lina_pieces(T, n, L), cs, list);
   return hipGetLastError();
 }

@@ -1,0 +1,57 @@
+// kda_verify_api.cpp -- C ABI of the drafted tokens' verification (include/kda.h, kda_verify_drafts).
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/kda.h"
+#include "kda_check.h"
+#include "kda_verify.h"
+
+namespace {
+
+int check_sizes(int B, int K, int V, int dtype) {
+  if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_DTYPE;
+  if (B < 0 || K < 0 || V < 1 || V > (1 << 30)) return KDA_ERR_SHAPE;
+  const int64_t tiles = (V + (int64_t)kda::kVerifyTile - 1) / kda::kVerifyTile;
+  return (int64_t)B * tiles > 0xFFFFFFFFll / 256 || (int64_t)B * (K + 1) > (int64_t(1) << 31) ? KDA_ERR_SHAPE : KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_verify_drafts_workspace_size(int B, int K, int V, int dtype) {
+  if (check_sizes(B, K, V, dtype) != KDA_OK) return 0;
+  return (size_t)B * ((V + (size_t)kda::kVerifyTile - 1) / kda::kVerifyTile) * 16;
+}
+
+int kda_verify_drafts(int B, int K, int V, int dtype, const void* target_probs, const int* drafts,
+                      const void* draft_probs, const float* u, const float* u_next, int* accepted, int* next_token,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_sizes(B, K, V, dtype);
+  if (rc) return rc;
+  if (B == 0) return KDA_OK;
+  if (!target_probs || (K > 0 && (!drafts || !u)) || !u_next || !accepted || !next_token || !workspace) return KDA_ERR_NULL;
+  const unsigned es = dtype == KDA_BF16 ? 2 : 4;
+  if (misaligned(target_probs, es) || misaligned(draft_probs, es) || misaligned(drafts, 4) || misaligned(u, 4) ||
+      misaligned(u_next, 4) || misaligned(accepted, 4) || misaligned(next_token, 4) || misaligned(workspace, 8))
+    return KDA_ERR_ALIGN;
+  const size_t need = kda_verify_drafts_workspace_size(B, K, V, dtype);
+  if (workspace_bytes < need) return KDA_ERR_WORKSPACE;
+  const int64_t n = (int64_t)B * K;
+  const Range in[] = {range_of(target_probs, (n + B) * V * es), range_of(draft_probs, draft_probs ? n * V * es : 0),
+                      range_of(drafts, drafts ? n * 4 : 0), range_of(u, u ? n * 4 : 0), range_of(u_next, (int64_t)B * 4)};
+  const Range out[] = {range_of(accepted, (int64_t)B * 4), range_of(next_token, (int64_t)B * 4),
+                       range_of(workspace, (int64_t)need)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return KDA_ERR_ALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(out[i], out[j])) return KDA_ERR_ALIAS;
+  }
+  const kda::VerifyArgs a{B,      K,        V,          (int)((V + (int64_t)kda::kVerifyTile - 1) / kda::kVerifyTile),
+                          target_probs, draft_probs, drafts, u, u_next, accepted, next_token, (double*)workspace,
+                          dtype == KDA_BF16, stream};
+  return kda::launch_verify(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+}  // extern "C"

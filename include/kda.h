@@ -30,7 +30,8 @@
  * Variants further down: the two-pass forward with a caller workspace, packed
  * variable-length batches, multi-token decode, Gated DeltaNet-2 gates and SFDA
  * complex gates, each with its backward; linear attention with a decay per head
- * (kda_lina_*); the norm and position rotation of q and k (kda_qk_norm_rope).
+ * (kda_lina_*); the delta rule with one decay per head (kda_gdr_*); verification of drafted
+ * tokens (kda_verify_drafts); the norm and position rotation of q and k (kda_qk_norm_rope).
  *
  * Conventions shared by all entry points
  *   - Every pointer except `shape` is a DEVICE pointer on the current HIP
@@ -506,6 +507,108 @@ int kda_lina_decode_step(const kda_shape* shape, int qk_heads, const void* q, co
                          const float* log_decay, int decay_per_head, float* state, void* o, void* stream);
 int kda_lina_decode_tokens(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
                            const float* log_decay, int decay_per_head, float* state, void* o, void* stream);
+
+/*
+ * The gated delta rule with one decay per head: the recurrence at the top with one gate for all
+ * key channels of a head, given as its logarithm, and q / k heads that serve several value heads,
+ *   S_t = e^(g_t) (I - beta_t k_t k_t^T) S_(t-1) + beta_t k_t v_t^T ,   o_t = S_t^T q_t ,
+ * chunked for whole sequences, recurrent for single tokens.  States have the layout of the other
+ * entry points.
+ *   qk_heads       : as for kda_lina_chunk_fwd
+ *   q, k, v, o     : as for kda_lina_chunk_fwd, both dtypes with every dk, dv in {64, 128}
+ *   log_decay      : [B, T, H] fp32 natural logarithms; g <= 0 is the intended range (not checked);
+ *                    -inf forgets the state exactly
+ *   beta           : [B, T, H], dtype of q, in [0, 2] with unit k as everywhere (not checked)
+ *   initial_state  : [B, H, dk, dv] fp32, or NULL for zeros
+ *   final_state    : [B, H, dk, dv] fp32, or NULL (not written); may equal initial_state
+ *   workspace      : kda_gdr_chunk_fwd_workspace_size(shape) bytes, 256-byte aligned: two lower
+ *                    triangles of each chunk of 64 tokens and head, the offsets of a packed batch,
+ *                    and where a batch has few chains the states its segments start from
+ * Arithmetic: fp32 sums, decays and states.  With bf16 inputs all that ends in the state goes through
+ * the matrix cores in terms that hold its 24 bits; o takes the state, r o q.k and beta (v - e^g S^T k)
+ * in terms that hold 16 bits, and is rounded once.  Inputs have to be finite: an infinity or NaN in a token
+ * spoils the outputs of its sequence from its chunk of 64 tokens on (other sequences and heads stay
+ * as they are).  Alignment: 16 bytes for q, k, v, o and the states, the element's for beta and
+ * log_decay.  Aliasing, packed batches (cu_seqlens, n_seqs, states of [n_seqs, H, dk, dv], token
+ * rows after the last offset not written) and errors as kda_lina_chunk_fwd(_varlen).
+ */
+size_t kda_gdr_chunk_fwd_workspace_size(const kda_shape* shape); /* 0 also if the shape is invalid */
+int kda_gdr_chunk_fwd(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                      const float* log_decay, const void* beta, const float* initial_state, void* o,
+                      float* final_state, void* workspace, size_t workspace_bytes, void* stream);
+size_t kda_gdr_chunk_fwd_varlen_workspace_size(const kda_shape* shape, int n_seqs);
+int kda_gdr_chunk_fwd_varlen(const kda_shape* shape, int qk_heads, const int* cu_seqlens, int n_seqs, const void* q,
+                             const void* k, const void* v, const float* log_decay, const void* beta,
+                             const float* initial_state, void* o, float* final_state, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of kda_gdr_chunk_fwd(_varlen): the gradients of
+ *   L = sum_t <d_o_t, o_t> + <d_final_state, S_T> .
+ *   d_o                 : [B, T, H, dv], dtype of q;  d_final_state : fp32 or NULL (zeros)
+ *   dq, dk, dv, d_beta  : outputs in the layout and dtype of q, k, v, beta (sums are fp32; q / k
+ *                         heads that serve several heads get the sum over them, rounded once).
+ *                         With bf16 inputs dq and dk take the states of both directions, dv,
+ *                         beta (v - e^g S^T k) and the scores rounded to bf16, d_beta the second
+ *                         of the vectors that it is the product of.
+ *   d_log_decay         : fp32 [B, T, H], or NULL when not wanted.  0 where e^g is under 2^-126,
+ *                         -inf among them.
+ *   d_initial_state     : fp32, or NULL when not wanted
+ *   workspace           : the size below, 256-byte aligned; besides the forward's it holds the states
+ *                         of both directions at every chunk
+ * Inputs have to be finite.  Token rows after the last offset of a packed batch are not written.  No
+ * output may overlap an input, another output or the workspace (KDA_ERR_ALIAS).  Results do not
+ * depend on timing: every sum has a fixed order.
+ */
+size_t kda_gdr_chunk_bwd_workspace_size(const kda_shape* shape); /* 0 if invalid */
+int kda_gdr_chunk_bwd(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                      const float* log_decay, const void* beta, const float* initial_state, const void* d_o,
+                      const float* d_final_state, void* dq, void* dk, void* dv, float* d_log_decay, void* d_beta,
+                      float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+size_t kda_gdr_chunk_bwd_varlen_workspace_size(const kda_shape* shape, int n_seqs);
+int kda_gdr_chunk_bwd_varlen(const kda_shape* shape, int qk_heads, const int* cu_seqlens, int n_seqs, const void* q,
+                             const void* k, const void* v, const float* log_decay, const void* beta,
+                             const float* initial_state, const void* d_o, const float* d_final_state, void* dq,
+                             void* dk, void* dv, float* d_log_decay, void* d_beta, float* d_initial_state,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The recurrent form: one token (q, k [B, qk_heads, dk]; v, o [B, H, dv]; log_decay, beta [B, H]), or
+ * shape->T tokens in order ([B, T, ...]), for every (b, h), the fp32 state [B, H, dk, dv] read once and
+ * updated in place.  Rules as kda_decode_step and kda_decode_tokens (16-byte aligned state, element
+ * alignment otherwise).  For tokens that may not stand (drafts):
+ *   counts : [B] int32 on the device, or NULL: of sequence b only the first counts[b] tokens (clamped to
+ *            [0, T]) are taken, o behind them is left as it was
+ *   update : 0 leaves the state as it is
+ *   q, o   : both NULL: the state alone goes on
+ */
+int kda_gdr_decode_step(const kda_shape* shape, int qk_heads, const void* q, const void* k, const void* v,
+                        const float* log_decay, const void* beta, float* state, void* o, void* stream);
+int kda_gdr_decode_tokens(const kda_shape* shape, int qk_heads, const int* counts, int update, const void* q,
+                          const void* k, const void* v, const float* log_decay, const void* beta, float* state,
+                          void* o, void* stream);
+
+/*
+ * Verification of drafted tokens.  Draft i of a sequence, x_i, stands while the ones before it do and
+ *   u_i q_i(x_i) < p_i(x_i) ;
+ * with n of them standing the next token is the lowest index whose running sum of weights passes
+ * u_next times their whole; the weights are max(p_n - q_n, 0) where draft n was refused, p_n where
+ * there is none (n == K, or x_n outside [0, V): padding).  All sums and products are fp64.
+ *   target_probs : [B, K + 1, V] p in dtype;  draft_probs : [B, K, V] q in dtype, or NULL: all of q_i
+ *                  is on x_i
+ *   drafts       : [B, K] int32;  u : [B, K], u_next : [B] fp32 in [0, 1) (a u_next outside draws the
+ *                  first or the last index that weighs anything)
+ *   accepted, next_token : [B] int32 outputs
+ *   workspace    : the size below, 8-byte aligned
+ * Entries that are negative or not finite weigh nothing (a NaN never lets a draft stand).  Weights that are
+ * all zero after a refusal give way to p_n; next_token is -1 where that weighs nothing either.
+ * Alignment: the elements'.  No output may overlap an input, another output or the workspace.  V <= 2^30;
+ * more than 2^24 pieces of 2,048 tokens are KDA_ERR_SHAPE.
+ */
+size_t kda_verify_drafts_workspace_size(int B, int K, int V, int dtype); /* 0 if invalid */
+int kda_verify_drafts(int B, int K, int V, int dtype, const void* target_probs, const int* drafts,
+                      const void* draft_probs, const float* u, const float* u_next, int* accepted, int* next_token,
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Queries and keys as the entry points above take them: each head's norm and the rotation by
