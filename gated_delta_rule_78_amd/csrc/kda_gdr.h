@@ -10,8 +10,9 @@ namespace kda {
 struct GdrWalk {
   LinaWalk walk;
   const void* beta = nullptr;   // [rows, H], element type of q
-  float* inv = nullptr;         // [chunks][H][kTriBlocks * 256]: (I + A o beta)^-1 of each chunk
+  float* inv = nullptr;         // [chunks][H][kTriBlocks * 256]: (I + A diag(beta))^-1 of each chunk
   float* score = nullptr;       // the same of P
+  float* token = nullptr;       // [chunks][H][kTokenFloats]: decays and strengths of each chunk's tokens
   float* transfer = nullptr;    // segments: [lina_ends][H][dk / 64][dk * 64], laid out as seg_state
   bool train = false;           // the backward's forward: leaves r, the chunks' states and do . o
   void* kept = nullptr;         // [chunks][H][dv / 64][64][dk]: the state each chunk meets, element type of q
@@ -19,6 +20,7 @@ struct GdrWalk {
   float* dots2 = nullptr;       // reverse: z . r, [dv / 64][H][rows]
 };
 
+constexpr int kTokenFloats = 3 * 64 + 4;
 constexpr int kTriBlocks = 10;  // 16 x 16 blocks of a chunk's lower triangle
 
 // chunks of a batch, as lina_pieces(.., 1) counts them

@@ -21,8 +21,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "kda_gdr.h"
-#include "kda_lina_tile.h"
+#include "kda_gdr_tile.h"
 
 namespace kda {
 
@@ -39,12 +38,6 @@ struct GdrParams {
   WalkParams p;  // p.w = a.walk
   int64_t chunks;
 };
-
-// 16 x 16 block (I, J) of a lower triangle.  A lane holds row n, columns 4 g .. 4 g + 3 of a block, in
-// memory and LDS lane after lane: a matrix-core operand is read, and a transposed accumulator tile
-// written, without a shuffle.
-__host__ __device__ constexpr int tri(int I, int J) { return I * (I + 1) / 2 + J; }
-constexpr int kTriUnits = kTriBlocks * 64;  // lane quads of a triangle
 
 // ---------------------------------------------------------------------------------------
 // N and P of every chunk
@@ -178,8 +171,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void gdr_prep_kernel(c
     r[3] = fast_exp2((ih - jh.w) + (il - jl.w));
   };
 
+  {  // what the walk needs of the tokens
+    float* tok = gp.a.token + slot * kTokenFloats;
+    tok[lane] = L.dec.row[lane];
+    tok[C + lane] = L.dec.col[lane];
+    tok[2 * C + lane] = L.beta[lane];
+    if (lane == 0) tok[3 * C] = L.dec.tot;
+  }
+
   // P: rows of block row I are q's (in reverse k's) against k's (q's)
-  f32x4_t M[kTriBlocks];
+  f32x4_t M[10];
 #pragma unroll
   for (int I = 0; I < 4; ++I) {
     Frag<T> fq[KS];
@@ -198,8 +199,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void gdr_prep_kernel(c
       float r[4];
       decay(bi, bj, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = bi != bj || 4 * g + i <= n ? a[i] * r[i] : 0.f;
-      score[tri(bi, bj) * 64] = make_float4(r[0], r[1], r[2], r[3]);
+      for (int i = 0; i < 4; ++i) a[i] = bi != bj || 4 * g + i <= n ? a[i] * r[i] : 0.f;
+      *(f32x4_t*)&score[tri(bi, bj) * 64] = a;
     }
   }
   // -A o beta, as row blocks
@@ -253,136 +254,26 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void gdr_prep_kernel(c
 // the walk
 // ---------------------------------------------------------------------------------------
 
-// fp32 values as matrix-core operands: themselves, or in bf16 terms (three hold all 24 bits)
-template <typename T, int N>
-struct Terms {
-  Frag<T> f[N];
-};
-template <typename T, int N>
-__device__ __forceinline__ void split(const f32x4_t& a, const f32x4_t& b, Terms<T, N>& t) {
-  if constexpr (sizeof(T) == 4) {
-    t.f[0].from_acc(a, b);
-  } else {
-    f32x4_t x = a, y = b;
-#pragma unroll
-    for (int m = 0; m < N; ++m) {
-      t.f[m].from_acc(x, y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] -= t.f[m].get(i);
-        y[i] -= t.f[m].get(4 + i);
-      }
-    }
-  }
-}
-// terms of the products of two split operands: all whose size is over 2^-24 of the first's
-template <typename T, int N, int M>
-__device__ __forceinline__ void mma_terms(f32x4_t& acc, const Terms<T, N>& a, const Terms<T, M>& b) {
-#pragma unroll
-  for (int o = (N > M ? N : M) - 1; o >= 0; --o)
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int j = 0; j < M; ++j)
-        if (i + j == o) mma(acc, a.f[i], b.f[j]);
-}
-template <typename T>
-constexpr int kAll = sizeof(T) == 2 ? 3 : 1;  // terms that hold a value's 24 bits
-template <typename T>
-constexpr int kMost = sizeof(T) == 2 ? 2 : 1;  // terms that hold 16 of them
-
-// A lane's base for the token fragments below: row 4 g + n / 4, quad n % 4.
-template <typename T, int D>
-__device__ __forceinline__ uint32_t pair_base(int lane) {
-  const int g = lane >> 4, n = lane & 15;
-  return sizeof(T) == 2 ? (uint32_t)Tile<T, D>::quad(4 * g + (n >> 2), n & 3) : 0u;
-}
-// slots 0-3 hold tokens 32 s + 4 g .., slots 4-7 tokens 32 s + 16 + 4 g .. of column c0 + n: the order in which
-// two accumulator tiles of 16 tokens hold theirs
-template <typename T, int D>
-__device__ __forceinline__ void pair_frag(Frag<T>& f, const char* t, uint32_t base, int c0, int s, int lane) {
-  if constexpr (sizeof(T) == 2) {
-#ifndef KDA_HOST_PASS
-    const char* p = t + 32 * s * Tile<T, D>::RB + (base ^ (c0 * 2));
-    const v4s_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p);
-    const v4s_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 16 * Tile<T, D>::RB));
-    const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
-    f.w[0] = x.x; f.w[1] = x.y; f.w[2] = y.x; f.w[3] = y.y;
-#endif
-  } else {
-    const int g = lane >> 4, c = c0 + (lane & 15);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      f.w[e] = *(const float*)(t + Tile<T, D>::quad(32 * s + 16 * (e >> 2) + 4 * g + (e & 3), c >> 2) + (c & 3) * 4);
-  }
-}
-
-// A triangle in LDS: N terms of a plane each (bf16), or fp32.
-template <typename T, int N>
-constexpr int kTriBytes = kTriUnits * 4 * (int)sizeof(T) * (sizeof(T) == 2 ? N : 1);
-
-// rows 16 t + n, columns of the block pair s (in the order of pair_frag's tokens); blocks above the diagonal are zero
-template <typename T, int N>
-__device__ __forceinline__ void tri_frag(Terms<T, N>& f, const char* p, int t, int s, int lane) {
-#pragma unroll
-  for (int x = 0; x < N; ++x) {
-    const char* at = p + x * kTriUnits * 4 * (int)sizeof(T) + lane * 4 * (int)sizeof(T);
-    const char* a = at + tri(t, 2 * s) * 256 * (int)sizeof(T);
-    const char* b = at + tri(t, 2 * s + 1) * 256 * (int)sizeof(T);
-    if (2 * s + 1 <= t) {
-      f.f[x].load4x2(a, b);
-    } else {
-      f.f[x].load4x2(a, a);
-#pragma unroll
-      for (int i = sizeof(T) == 2 ? 2 : 4; i < (sizeof(T) == 2 ? 4 : 8); ++i) f.f[x].w[i] = 0;
-    }
-  }
-}
-
 template <typename T, int DK, int MODE>
 struct WalkLds {
   static constexpr int NP = MODE == kFwd ? kMost<T> : kAll<T>;  // terms of P
-  static constexpr int K = 0, V = K + Tile<T, DK>::BYTES, N = V + Tile<T, VT>::BYTES, Q = N + kTriBytes<T, kAll<T>>;
-  static constexpr int P = Q + (MODE == kSegFwd ? 0 : Tile<T, DK>::BYTES);
+  static constexpr int K = 0, V = K + RowTile<T, DK>::BYTES, N = V + RowTile<T, VT>::BYTES, Q = N + kTriBytes<T, kAll<T>>;
+  static constexpr int P = Q + (MODE == kSegFwd ? 0 : RowTile<T, DK>::BYTES);
   static constexpr int SIZE = P + (MODE == kSegFwd ? 0 : kTriBytes<T, NP>);
-  static constexpr int NBUF = 2 * SIZE <= 150 * 1024 ? 2 : 1;
+  static constexpr int NBUF = 2 * SIZE <= 152 * 1024 ? 2 : 1;
   static constexpr int BYTES = NBUF * SIZE;
 };
 
-// fp32 quads of a triangle on their way from memory to LDS, in N terms
-template <typename T, int N>
-struct StageTri {
-  static constexpr int R = (kTriUnits + NT - 1) / NT;
-  u32x4_t r[R];
-  __device__ __forceinline__ void load(const void* base, size_t slot, int tid) {
-    const Rows b((const char*)base + slot * (kTriUnits * 16), kTriUnits * 16);
+// fn(ct, i, element) over a thread's entries of a [dk, dv] state: row channel(ct, 4 g + i), column 16 wave + n
+template <int DK, typename F>
+__device__ __forceinline__ void each_entry(const LinaWalk& w, const Chain& ch, int wave, int lane, F fn) {
+  const int g = lane >> 4, vc = ch.vt * VT + 16 * wave + (lane & 15);
+  const size_t b0 = ((size_t)ch.sq * w.H + ch.h) * (size_t)DK * w.dv + vc;
 #pragma unroll
-    for (int i = 0; i < R; ++i) r[i] = b.load16((tid + NT * i) * 16);
-  }
-  __device__ __forceinline__ void store(char* t, int tid) const {
+  for (int ct = 0; ct < DK / 16; ++ct)
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int u = tid + NT * i;
-      if (u >= kTriUnits) break;
-      if constexpr (sizeof(T) == 4) {
-        *(u32x4_t*)(t + u * 16) = r[i];
-      } else {
-        float x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(r[i][j]);
-#pragma unroll
-        for (int m = 0; m < N; ++m) {
-          const uint32_t a = pack_bf16x2(x[0], x[1]), b = pack_bf16x2(x[2], x[3]);
-          *(uint2*)(t + m * kTriUnits * 8 + u * 8) = make_uint2(a, b);
-          x[0] -= __uint_as_float(a << 16);
-          x[1] -= __uint_as_float(a & 0xFFFF0000u);
-          x[2] -= __uint_as_float(b << 16);
-          x[3] -= __uint_as_float(b & 0xFFFF0000u);
-        }
-      }
-    }
-  }
-};
+    for (int i = 0; i < 4; ++i) fn(ct, i, b0 + (size_t)(channel(ct, 4 * g) + i) * w.dv);
+}
 
 // Where a walk's segment slots lie: [piece][H][value tiles].
 __device__ __forceinline__ size_t seg_at(const LinaWalk& w, const Chain& ch, int64_t piece, int vt) {
@@ -402,7 +293,7 @@ __device__ __forceinline__ void first_state(const GdrParams& gp, const Chain& ch
 #pragma unroll
     for (int ct = 0; ct < DK / 16; ++ct) S[ct] = from[ct * NT + tid];
   } else if (w.s0) {
-    each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
+    each_entry<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
   }
 }
 
@@ -421,23 +312,29 @@ __device__ __forceinline__ void gdr_anchor(const WalkParams& p, const Chain& ch,
       for (int i = 0; i < 4; ++i) d = fmaf(x[i], S[ct][i], d);
     }
   } else if (w.snap0) {
-    each_state<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { d = fmaf(w.snap0[at], S[ct][i], d); });
+    each_entry<DK>(w, ch, tid >> 6, tid & 63, [&](int ct, int i, size_t at) { d = fmaf(w.snap0[at], S[ct][i], d); });
   }
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) d += __shfl_xor(d, off);
   if ((tid & 63) == 0) w.anchor[ch.at(p, ch.anchor(p, c)) * 4 + (tid >> 6)] = expf(ch.decay_log(w, ch.lo + (int64_t)c * C)) * d;
 }
 
-// What a chunk's tokens need besides the tiles.
+// What a chunk's tokens need besides the tiles, as gdr_prep_kernel leaves it.
 struct TokenLds {
-  Decays dec;
+  float row[C];   // decay from the chunk's start to the token
+  float col[C];   // from the token to the chunk's end
   float beta[C];
+  float tot;      // the whole chunk
+  float pad[3];
 };
+static_assert(sizeof(TokenLds) == kTokenFloats * 4, "as in memory");
 
 // One chain: four waves keep the state (16 value columns each, fp32 accumulators that serve as operands), four
 // fetch the next chunk's tiles.  Products run as [token][value] where the next product takes them along the
 // tokens (K S, N ., P .), so that no value leaves its lane between them, and transposed where they are
-// stored (four neighbouring columns of one token to a lane).
+// stored (four neighbouring columns of one token to a lane).  A state wave has its matrix unit to itself, and its products
+// wait for each other: operands are read a group of products ahead, and what the state does not wait for (P u, the
+// outputs) stands between what it does.
 //
 // Precision (bf16 inputs): what ends in the state or in an fp32 output goes through the matrix cores in
 // three bf16 terms (all 24 bits): S against k, N and what it multiplies, b o r against k.  The forward's
@@ -446,11 +343,11 @@ template <typename T, int DK, int MODE>
 __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
   typedef WalkLds<T, DK, MODE> Lds;
   constexpr bool REV = is_rev(MODE), SEG = is_seg(MODE);
-  constexpr bool HAS_Q = MODE != kSegFwd, HAS_P = HAS_Q;
+  constexpr bool HAS_Q = MODE != kSegFwd, HAS_P = HAS_Q, OUT = MODE == kFwd || MODE == kTrain, DOTS = MODE == kTrain || MODE == kRev;
   constexpr int A3 = kAll<T>, CT = DK / 16, KS = DK / 32, NBUF = Lds::NBUF;
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) TokenLds tok[2];
-  __shared__ float sdot[MODE == kTrain || MODE == kRev ? 2 : 1][4][C], sdot2[MODE == kRev ? 2 : 1][4][C];
+  __shared__ float sdot[DOTS ? 2 : 1][4][C], sdot2[MODE == kRev ? 2 : 1][4][C];
   const WalkParams& p = gp.p;
   const LinaWalk& w = p.w;
   const int tid = threadIdx.x & (NT - 1), lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
@@ -465,45 +362,43 @@ __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
   // the first of this sequence's chunks in the tables of N and P
   const int64_t base = w.cs ? ch.lo / C + ch.sq : (int64_t)ch.sq * ch.nch;
   auto slot = [&](int it) { return (size_t)(base + chunk(it)) * w.H + ch.h; };
+  const Residual res;
 
   if (threadIdx.x >= NT) {
     if (steps == 0) return;
     const Operand<T> q(w.q, w, ch.h, DK, 0), k(w.k, w, ch.h, DK, 0), v(w.v, w, ch.h, w.dv, (ident ? 0 : ch.vt) * VT);
-    Stage<T, DK> rk, rq;
-    Stage<T, VT> rv;
-    StageTri<T, A3> rn;
-    StageTri<T, Lds::NP> rp;
-    float rg = 0.f, rb = 0.f;
-    auto fetch = [&](int it) {
+    struct Tiles {
+      StageRows<T, DK> k, q;
+      StageRows<T, VT> v;
+      StageTri<T, A3> n;
+      StageTri<T, Lds::NP> p;
+      u32x4_t t;  // the last wave's
+    };
+    // bf16: two chunks are on their way, because from memory under load a tile takes longer than a step.
+    constexpr int SETS = sizeof(T) == 2 ? 2 : 1;
+    Tiles ra, rb;
+    auto fetch = [&](Tiles& r, int it) {
       const int c = chunk(it);
       const int64_t t = ch.lo + (int64_t)c * C;
       const uint32_t have = ch.rows(c);
-      if (wave == 0) {
-        rg = row_decay<REV>(w, ch, c, lane);
-        const int64_t tb = t + (REV ? C - 1 - lane : lane);
-        rb = tb < ch.hi ? Elem<T>::load(gp.a.beta, (size_t)tb * w.H + ch.h) : 0.f;
-      }
-      rk.load(k.rows(t, have), k.step, REV, tid);
-      rv.load(v.rows(t, ident ? 0 : have), v.step, REV, tid);
-      rn.load(gp.a.inv, slot(it), tid);
-      if constexpr (HAS_Q) rq.load(q.rows(t, have), q.step, REV, tid);
-      if constexpr (HAS_P) rp.load(gp.a.score, slot(it), tid);
+      if (wave == 3) r.t = Rows(gp.a.token + slot(it) * kTokenFloats, kTokenFloats * 4).load16(lane * 16);
+      r.k.load(k.rows(t, have), k.step, REV, tid);
+      r.v.load(v.rows(t, ident ? 0 : have), v.step, REV, tid);
+      r.n.load(gp.a.inv, slot(it), tid);
+      if constexpr (HAS_Q) r.q.load(q.rows(t, have), q.step, REV, tid);
+      if constexpr (HAS_P) r.p.load(gp.a.score, slot(it), tid);
     };
-    auto put = [&](int it) {
+    auto put = [&](const Tiles& r, int it) {
       char* b = buf(it);
-      if (wave == 0) {
-        TokenLds& x = tok[it & 1];
-        x.beta[lane] = rb;
-        chunk_decays(x.dec, rg, lane);
-      }
-      rk.store(b + Lds::K, tid);
-      rv.store(b + Lds::V, tid);
-      rn.store(b + Lds::N, tid);
-      if constexpr (HAS_Q) rq.store(b + Lds::Q, tid);
-      if constexpr (HAS_P) rp.store(b + Lds::P, tid);
+      if (wave == 3 && lane < kTokenFloats / 4) *(u32x4_t*)((char*)&tok[it & 1] + lane * 16) = r.t;
+      r.k.store(b + Lds::K, tid);
+      r.v.store(b + Lds::V, tid);
+      r.n.store(res, b + Lds::N, tid);
+      if constexpr (HAS_Q) r.q.store(b + Lds::Q, tid);
+      if constexpr (HAS_P) r.p.store(res, b + Lds::P, tid);
     };
     auto dots = [&](int it) {  // a step's, once its waves are done
-      if constexpr (MODE == kTrain || MODE == kRev) {
+      if constexpr (DOTS) {
         if (wave == 1) store_dots<kDotRow, REV>(p, ch, chunk(it), sdot[it & 1], sdot[0][0], lane);
         if constexpr (MODE == kRev) {
           if (wave == 2) {
@@ -515,23 +410,30 @@ __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
         }
       }
     };
-    fetch(0);
-    put(0);
-    if (steps > 1) fetch(1);
+    fetch(ra, 0);
+    if (SETS == 2 && steps > 1) fetch(rb, 1);
+#pragma unroll
+    for (int x = 0; x < NBUF; ++x) {
+      tri_clear<T, A3>(smem + x * Lds::SIZE + Lds::N, tid);
+      if constexpr (HAS_P) tri_clear<T, Lds::NP>(smem + x * Lds::SIZE + Lds::P, tid);
+    }
+    put(ra, 0);
+    if (steps > SETS) fetch(ra, SETS);
     lds_barrier();
-    for (int it = 0; it < steps; ++it) {
-      if constexpr (NBUF == 2) {
-        if (it + 1 < steps) put(it + 1);
-        if (it + 2 < steps) fetch(it + 2);
-        if (it > 0) dots(it - 1);
-      }
-      lds_barrier();
+    auto step = [&](Tiles& r, int it) {  // r: chunk it + 1
       if constexpr (NBUF == 1) {
-        if (it + 1 < steps) put(it + 1);
-        if (it + 2 < steps) fetch(it + 2);
-        dots(it);
         lds_barrier();
+        dots(it);
       }
+      if (it + 1 < steps) put(r, it + 1);
+      if (it + 1 + SETS < steps) fetch(r, it + 1 + SETS);
+      if (NBUF == 2 && it > 0) dots(it - 1);
+      lds_barrier();
+    };
+    for (int it = 0; it < steps; it += 2) {
+      if constexpr (SETS == 2) step(rb, it);
+      else step(ra, it);
+      if (it + 1 < steps) step(ra, it + 1);
     }
     if constexpr (NBUF == 2) dots(steps - 1);
     return;
@@ -542,7 +444,8 @@ __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[ct][i] = ident && 16 * ct + 4 * g + i == (ch.vt - nv) * VT + 16 * wave + n ? 1.f : 0.f;
+      for (int i = 0; i < 4; ++i)
+        S[ct][i] = ident && channel(ct, 4 * g) + i == (ch.vt - nv) * VT + 16 * wave + n ? 1.f : 0.f;
   } else {
     first_state<DK>(gp, ch, REV, tid, S);
   }
@@ -551,10 +454,16 @@ __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
   auto fetch_dots = [&](int it) {
     const int c = chunk(it);
     const int64_t t = ch.lo + (int64_t)c * C;
-    if constexpr (MODE == kTrain || MODE == kRev) xd.load(x.rows(t, ch.rows(c)), x.step, REV, wave, lane);
+    if constexpr (DOTS) xd.load(x.rows(t, ch.rows(c)), x.step, REV, wave, lane);
     if constexpr (MODE == kRev) rd.load(xr.rows(t, ch.rows(c)), xr.step, REV, wave, lane);
   };
-  const uint32_t rb = row_base<T, DK, false>(lane), kb = pair_base<T, DK>(lane), vb = pair_base<T, VT>(lane);
+  const RowAt<T, DK> rows(lane);
+  const ColAt<T, DK, true> cols(lane);
+  const ColAt<T, VT, false> vals(lane);
+  // The state's operands, 32 channels each, made as soon as the update before is through with them.
+  Terms<T, A3> fs[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) split(res, S[2 * s], S[2 * s + 1], fs[s]);
   if (steps > 0) {
     fetch_dots(0);
     lds_barrier();
@@ -564,109 +473,189 @@ __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
     const char* b = buf(it);
     const TokenLds& tl = tok[it & 1];
     const char *sK = b + Lds::K, *sQ = b + Lds::Q, *sV = b + Lds::V, *sN = b + Lds::N, *sP = b + Lds::P;
-    if constexpr (MODE == kTrain || MODE == kRev) {
-      // the state this chunk meets, as rows of value columns
-      T* to = (T*)gp.a.kept + (((size_t)(base + c) * w.H + ch.h) * nv + ch.vt) * (size_t)(VT * DK) + (16 * wave + n) * DK + 4 * g;
+    // operands a group of products ahead
+    Frag<T> fk[2][KS], fq[2][KS], fv[2];
+    auto load_rows = [&](int t) {
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const float s4[4] = {S[ct][0], S[ct][1], S[ct][2], S[ct][3]};
-        st_quad<T>((char*)(to + 16 * ct), s4);
+      for (int s = 0; s < KS; ++s) rows.load(fk[t & 1][s], sK, 16 * t, s);
+      if constexpr (OUT)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) rows.load(fq[t & 1][s], sQ, 16 * t, s);
+    };
+    load_rows(0);
+    f32x4_t rw[4], bt[4], cw[4];
+    float rn[4];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) vals.load(fv[y], sV, wave, y, lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) rw[t] = *(const f32x4_t*)&tl.row[16 * t + 4 * g];
+    if constexpr (DOTS) {
+      // the state this chunk meets, as rows of value columns
+      T* to = (T*)gp.a.kept + (((size_t)(base + c) * w.H + ch.h) * nv + ch.vt) * (size_t)(VT * DK) + (16 * wave + n) * DK + 8 * g;
+#pragma unroll
+      for (int c2 = 0; c2 < KS; ++c2) {
+        const float s8[8] = {S[2 * c2][0],     S[2 * c2][1],     S[2 * c2][2],     S[2 * c2][3],
+                             S[2 * c2 + 1][0], S[2 * c2 + 1][1], S[2 * c2 + 1][2], S[2 * c2 + 1][3]};
+        st_row8<T>((char*)(to + 32 * c2), s8);
       }
       if (MODE == kTrain && c > 0 && c % lina_keep(w.bf16) == 0) store_snap<DK>(p, ch, c, tid, S);
     }
-    // K S as [token][value]; Q S as [value][token]
-    f32x4_t kS[4], o[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) kS[t] = o[t] = zero4();
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      Terms<T, A3> fs;
-      split(S[2 * s], S[2 * s + 1], fs);
-#pragma unroll
-      for (int t2 = 0; t2 < 4; t2 += 2) {
-        Frag<T> f[2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) row_frag<T>(f[y], sK, rows_at<T, DK, false>(rb, 16 * (t2 + y)), s);
-#pragma unroll
-        for (int m = 0; m < A3; ++m)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) mma(kS[t2 + y], f[y], fs.f[m]);
-        if constexpr (MODE == kFwd || MODE == kTrain) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) row_frag<T>(f[y], sQ, rows_at<T, DK, false>(rb, 16 * (t2 + y)), s);
-#pragma unroll
-          for (int m = 0; m < (MODE == kTrain ? A3 : kMost<T>); ++m)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) mma(o[t2 + y], fs.f[m], f[y]);
-        }
-      }
-    }
-    Frag<T> fv[2];  // v (in reverse d_o) along the tokens
-#pragma unroll
-    for (int s = 0; s < 2; ++s) pair_frag<T, VT>(fv[s], sV, vb, 16 * wave, s, lane);
-    f32x4_t x0[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float4 r4 = *(const float4*)&tl.dec.row[16 * t + 4 * g];
-      const float rw[4] = {r4.x, r4.y, r4.z, r4.w};
+    // x0 = V - e^G o K S as [token][value] (in reverse e^G' o K R + P' d_o); Q S as [value][token]
+    f32x4_t kS[4], o[4], x0[4];
+    Terms<T, A3> fx[2], fn[4];
+    Terms<T, Lds::NP> fp[4];
+    auto from_values = [&](int t) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float y = rw[i] * kS[t][i];
+        const float y = rw[t][i] * kS[t][i];
         x0[t][i] = REV ? y : fv[t >> 1].get((t & 1) * 4 + i) - y;
       }
-    }
-    if constexpr (REV) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
+      if constexpr (REV)
 #pragma unroll
         for (int s = 0; s <= t / 2; ++s) {
-          Terms<T, Lds::NP> fp;
-          tri_frag(fp, sP, t, s, lane);
+          tri_frag(fp[0], sP, t, s, lane);
 #pragma unroll
-          for (int m = Lds::NP - 1; m >= 0; --m) mma(x0[t], fp.f[m], fv[s]);
+          for (int m = Lds::NP - 1; m >= 0; --m) mma(x0[t], fp[0].f[m], fv[s]);
         }
-    }
-    // r = N x0 (z in reverse)
-    Terms<T, A3> fx[2];
+    };
 #pragma unroll
-    for (int s = 0; s < 2; ++s) split(x0[2 * s], x0[2 * s + 1], fx[s]);
+    for (int t = 0; t < 4; ++t) {
+      if (t < 3) {
+        load_rows(t + 1);
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) tri_frag(fn[y], sN, y, 0, lane);
+      }
+      if (t == 2) from_values(0);
+      if (t == 3) {
+        from_values(1);
+        split(res, x0[0], x0[1], fx[0]);
+      }
+      kS[t] = o[t] = zero4();
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int m = 0; m < A3; ++m) mma(kS[t], fk[t & 1][s], fs[s].f[m]);
+      if constexpr (OUT)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int m = 0; m < (MODE == kTrain ? A3 : kMost<T>); ++m) mma(o[t], fs[s].f[m], fq[t & 1][s]);
+      if (t == 3) made(fx[0]);
+      in_turn();
+    }
+    // r = N x0 (z in reverse): the first 32 columns of N, then the last; rt: [value][token], to store it
     f32x4_t r[4], rt[4];
+    Terms<T, A3> fn2[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) tri_frag(fn2[t], sN, 2 + t, 1, lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) bt[t] = *(const f32x4_t*)&tl.beta[16 * t + 4 * g];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       r[t] = rt[t] = zero4();
-#pragma unroll
-      for (int s = 0; s <= t / 2; ++s) {
-        Terms<T, A3> fn;
-        tri_frag(fn, sN, t, s, lane);
-        mma_terms(r[t], fn, fx[s]);
-        if constexpr (MODE == kTrain || MODE == kRev) mma_terms(rt[t], fx[s], fn);  // [value][token], to store it
-      }
+      mma_terms(r[t], fn[t], fx[0]);
+      if constexpr (DOTS) mma_terms(rt[t], fx[0], fn[t]);
     }
-    // u = b o r (y in reverse)
+    from_values(2);
+    from_values(3);
+    split(res, x0[2], x0[3], fx[1]);
+    made(fx[1]);
+    in_turn();
+    // u = b o r (y in reverse), and what enters the state
+    constexpr int NU = MODE == kTrain ? A3 : kMost<T>;
     f32x4_t u[4];
+    Terms<T, A3> fy[2], fz[2];
+    Terms<T, NU> fu[2];
+    const float tot = tl.tot;
+    auto weigh = [&](int s) {
+      f32x4_t y[2], z[2];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float4 b4 = *(const float4*)&tl.beta[16 * t + 4 * g];
-      u[t][0] = b4.x * r[t][0];
-      u[t][1] = b4.y * r[t][1];
-      u[t][2] = b4.z * r[t][2];
-      u[t][3] = b4.w * r[t][3];
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u[2 * s + j][i] = bt[2 * s + j][i] * r[2 * s + j][i];
+          y[j][i] = (REV ? -cw[2 * s + j][i] : cw[2 * s + j][i]) * u[2 * s + j][i];
+          if constexpr (REV) z[j][i] = cw[2 * s + j][i] * fv[s].get(4 * j + i);
+        }
+      split(res, y[0], y[1], fy[s]);
+      made(fy[s]);
+      if constexpr (OUT) {
+        split(res, u[2 * s], u[2 * s + 1], fu[s]);
+        made(fu[s]);
+      }
+      if constexpr (REV) {
+        split(res, z[0], z[1], fz[s]);
+        made(fz[s]);
+      }
+    };
+#pragma unroll
+    for (int t = 0; t < 4; ++t) cw[t] = *(const f32x4_t*)&tl.col[16 * t + 4 * g];
+    if constexpr (OUT) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) tri_frag(fp[t], sP, t, 0, lane);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) rn[t] = tl.row[16 * t + n];
     }
-    if constexpr (MODE == kFwd || MODE == kTrain) {
-      constexpr int NU = MODE == kTrain ? A3 : kMost<T>;
-      scale_rows(o, tl.dec, lane);
+#pragma unroll
+    for (int t = 2; t < 4; ++t) {
+      mma_terms(r[t], fn2[t - 2], fx[1]);
+      if constexpr (DOTS) mma_terms(rt[t], fx[1], fn2[t - 2]);
+    }
+    weigh(0);
+    if constexpr (OUT)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][i] *= rn[t];
+    in_turn();
+    // o += P u, the first 32 columns of P, while the second half of what enters the state is made
+    Frag<T> fc[2][2], fd[2][2];
+    auto load_cols = [&](int ct) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        Terms<T, NU> fu;
-        split(u[2 * s], u[2 * s + 1], fu);
-#pragma unroll
-        for (int t = 2 * s; t < 4; ++t) {
-          Terms<T, Lds::NP> fp;
-          tri_frag(fp, sP, t, s, lane);
-          mma_terms(o[t], fu, fp);
-        }
+        cols.load(fc[ct & 1][s], sK, ct, s, lane);
+        if constexpr (REV) cols.load(fd[ct & 1][s], sQ, ct, s, lane);
       }
+    };
+    load_cols(0);
+    if constexpr (OUT)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) mma_terms(o[t], fu[0], fp[t]);
+    weigh(1);
+    in_turn();
+    // S <- e^{G_C} S + K^T y (in reverse + Q^T z)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      if (ct + 1 < CT) {
+        load_cols(ct + 1);
+      } else {
+        if constexpr (OUT)
+#pragma unroll
+          for (int t = 2; t < 4; ++t) tri_frag(fp[t], sP, t, 1, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[ct][i] *= tot;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int m = 0; m < A3; ++m) mma(S[ct], fc[ct & 1][s], fy[s].f[m]);
+      if constexpr (REV)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int m = 0; m < A3; ++m) mma(S[ct], fd[ct & 1][s], fz[s].f[m]);
+      if (ct >= 2 && ct % 2 == 0) {
+        split(res, S[ct - 2], S[ct - 1], fs[ct / 2 - 1]);
+        made(fs[ct / 2 - 1]);
+      }
+      in_turn();
     }
+    if constexpr (OUT)
+#pragma unroll
+      for (int t = 2; t < 4; ++t) mma_terms(o[t], fu[1], fp[t]);
+    split(res, S[CT - 2], S[CT - 1], fs[KS - 1]);
+    made(fs[KS - 1]);
     if constexpr (MODE == kFwd) store_out<T, false>(o, w, ch, c, wave, lane);
     if constexpr (MODE == kTrain) {
       xd.dot(o, sdot[it & 1][wave], lane);
@@ -676,56 +665,15 @@ __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
       rd.dot(rt, sdot2[it & 1][wave], lane);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const float bt = tl.beta[16 * t + n];
+        const float bn = tl.beta[16 * t + n];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rt[t][i] *= bt;
+        for (int i = 0; i < 4; ++i) rt[t][i] *= bn;
       }
       xd.dot(rt, sdot[it & 1][wave], lane);
       store_out<T, true>(rt, w, ch, c, wave, lane);
     }
-    if constexpr (MODE == kTrain || MODE == kRev)
+    if constexpr (DOTS)
       if (it + 1 < steps) fetch_dots(it + 1);
-    // the state
-    const float tot = tl.dec.tot;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) S[ct][i] *= tot;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      f32x4_t y[2], z[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4 c4 = *(const float4*)&tl.dec.col[32 * s + 16 * j + 4 * g];
-        const float cw[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[j][i] = (REV ? -cw[i] : cw[i]) * u[2 * s + j][i];
-          if constexpr (REV) z[j][i] = cw[i] * fv[s].get(4 * j + i);
-        }
-      }
-      Terms<T, A3> fy, fz;
-      split(y[0], y[1], fy);
-      if constexpr (REV) split(z[0], z[1], fz);
-#pragma unroll
-      for (int c2 = 0; c2 < CT; c2 += 2) {
-        Frag<T> f[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) pair_frag<T, DK>(f[j], sK, kb, 16 * (c2 + j), s, lane);
-#pragma unroll
-        for (int m = 0; m < A3; ++m)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) mma(S[c2 + j], f[j], fy.f[m]);
-        if constexpr (REV) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) pair_frag<T, DK>(f[j], sQ, kb, 16 * (c2 + j), s, lane);
-#pragma unroll
-          for (int m = 0; m < A3; ++m)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mma(S[c2 + j], f[j], fz.f[m]);
-        }
-      }
-    }
     if constexpr (MODE == kRev)
       if (w.anchor && c % lina_keep(w.bf16) == 0) gdr_anchor<DK>(p, ch, c, tid, S);
     lds_barrier();
@@ -737,8 +685,9 @@ __global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
                       : w.seg_state + seg_at(w, ch, piece, ch.vt) * (DK * VT);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) ((f32x4_t*)at)[ct * NT + tid] = S[ct];
-  } else {
-    store_state<DK, REV>(p, ch, tid, S);
+  } else if (w.sT && ch.tail) {  // a reverse walk's state is the gradient after the first token's decay
+    const float d = REV && ch.nch > 0 ? expf(ch.decay_log(w, ch.lo)) : 1.f;
+    each_entry<DK>(w, ch, wave, lane, [&](int ct, int i, size_t at) { w.sT[at] = S[ct][i] * d; });
   }
 }
 
@@ -758,7 +707,7 @@ __global__ __launch_bounds__(NT) void gdr_link_kernel(const GdrParams gp, bool r
   f32x4_t S[CT];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) S[ct] = zero4();
-  if (w.s0) each_state<DK>(w, ch, wave, lane, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
+  if (w.s0) each_entry<DK>(w, ch, wave, lane, [&](int ct, int i, size_t at) { S[ct][i] = w.s0[at]; });
   auto put = [&](int64_t piece) {
     f32x4_t* to = (f32x4_t*)(w.seg_state + seg_at(w, ch, piece, ch.vt) * (DK * VT));
 #pragma unroll
@@ -785,7 +734,7 @@ __global__ __launch_bounds__(NT) void gdr_link_kernel(const GdrParams gp, bool r
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int kt = 0; kt < CT; ++kt) mm16(X[ct], *(const f32x4_t*)&sM[(16 * ct + n) * LD + 16 * kt + 4 * g], S[kt]);
+      for (int kt = 0; kt < CT; ++kt) mm16(X[ct], *(const f32x4_t*)&sM[(16 * ct + n) * LD + channel(kt, 4 * g)], S[kt]);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) S[ct] = X[ct];
     put(piece);

@@ -86,21 +86,22 @@ Plan gdr_plan(const kda_shape& s, int n_seqs) {
 bool launchable(const Plan& p, const kda_shape& s, int qk_heads) {
   const int tiles = (s.dv + s.dk) / 64;
   return ((p.nseg * qk_heads + 7) / 8 * 8) * (s.H / qk_heads) * tiles <= 0xFFFFFFFFll / 512 &&
-         p.chunks * ((s.H + 3) / 4) <= 0xFFFFFFFFll / 256 && p.chunks * qk_heads <= 0xFFFFFFFFll / 512;
+         p.chunks * ((s.H + 3) / 4) <= 0xFFFFFFFFll / 256 && p.chunks * qk_heads <= 0xFFFFFFFFll / 256;
 }
 
 // What either direction's walk needs.
 struct Layout {
   Plan plan;
-  size_t off_score, off_seg, off_transfer, off_cs, off_list, bytes;
+  size_t off_score, off_token, off_seg, off_transfer, off_cs, off_list, bytes;
 };
 
 Layout layout(const kda_shape& s, int n_seqs) {
   Layout l;
   l.plan = gdr_plan(s, n_seqs);
-  const size_t tri = (size_t)l.plan.chunks * s.H * kda::kTriBlocks * 256;
-  l.off_score = up(tri * 4);
-  l.off_seg = up(l.off_score + tri * 4);
+  const size_t tri = (size_t)l.plan.chunks * s.H * kda::kTriBlocks * 256 * 4;
+  l.off_score = up(tri);
+  l.off_token = up(l.off_score + tri);
+  l.off_seg = up(l.off_token + (size_t)l.plan.chunks * s.H * kda::kTokenFloats * 4);
   l.off_transfer = up(l.off_seg + (size_t)l.plan.states * s.H * s.dk * s.dv * 4);
   l.off_cs = up(l.off_transfer + (size_t)l.plan.ends * s.H * s.dk * s.dk * 4);
   l.off_list = up(l.off_cs + (n_seqs >= 0 ? ((size_t)n_seqs + 2) * 4 : 0));
@@ -123,6 +124,7 @@ int start(kda::GdrWalk& a, const kda_shape& s, const Layout& l, int n_seqs, cons
   w.seg_state = (float*)(ws + l.off_seg);
   a.inv = (float*)ws;
   a.score = (float*)(ws + l.off_score);
+  a.token = (float*)(ws + l.off_token);
   a.transfer = (float*)(ws + l.off_transfer);
   if (n_seqs < 0) return KDA_OK;
   w.cs = (const int*)(ws + l.off_cs);

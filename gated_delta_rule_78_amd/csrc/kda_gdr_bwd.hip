@@ -5,12 +5,11 @@
 //   E_ij = D_ij do_i . u_j (j <= i),   F_ij = D_ij y_i . u_j (j < i),
 //   dq = E K + e^G o (do S^T),
 //   dk = E^T Q - (F + F^T) K - e^G o (y S^T) + e^G' o (u R^T).
-// One workgroup makes dq and dk of one chunk and shared head, summed over the heads it serves in registers: a
-// wave half of the channels of one block of 16 tokens, in 16 x 16 tiles with rows = channels, columns = tokens,
-// so that a lane stores four neighbouring channels.  Operands go through LDS, 64 value columns at a time, the
+// One workgroup makes dq and dk of one chunk and shared head, summed over the heads it serves in registers: wave
+// w block w of 16 tokens, in 16 x 16 tiles with rows = channels, columns = tokens, so that a lane stores four
+// neighbouring channels.  Operands go through LDS, 64 value columns at a time, the
 // two states one after the other through the same tile: 72 KB (bf16), two workgroups to a compute unit.
-#include "kda_gdr.h"
-#include "kda_lina_tile.h"
+#include "kda_gdr_tile.h"
 
 namespace kda {
 
@@ -27,14 +26,6 @@ struct GradLds {
   static constexpr int DO = S + Tile<T, DK>::BYTES, Y = DO + Tile<T, VT>::BYTES, U = Y + Tile<T, VT>::BYTES;
   static constexpr int BYTES = U + Tile<T, VT>::BYTES;
 };
-
-// Between two steps of an unrolled loop: the compiler would otherwise read the operands of all of them first and
-// spill what it holds.
-__device__ __forceinline__ void in_turn() {
-#ifndef KDA_HOST_PASS
-  __builtin_amdgcn_sched_barrier(0);
-#endif
-}
 
 // slots 0-3 hold rows 32 s + 4 g .., slots 4-7 rows 32 s + 16 + 4 g .. of column c0 + n
 template <typename T, int D>
@@ -74,9 +65,9 @@ __device__ __forceinline__ void scale_stage(Stage<T, D>& r, const float* by, int
 }
 
 template <typename T, int DK>
-__global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp) {
+__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void gdr_grad_kernel(const GradParams gp) {
   typedef GradLds<T, DK> Lds;
-  constexpr int CT = DK / 32;  // channel tiles of a wave
+  constexpr int CT = DK / 16;
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) Decays dec, back;
   __shared__ float beta[C];
@@ -84,8 +75,8 @@ __global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp
   const LinaWalk& w = f.walk;
   // The wave's number in a scalar: branches on it are jumps.  Under an execution mask, as the compiler may
   // put short ones, matrix instructions would run all the same.
-  const int tid = threadIdx.x & (NT - 1), lane = tid & 63, g = lane >> 4, n = lane & 15;
-  const int wave = (int)uniform64(tid >> 6), half = (int)uniform64(threadIdx.x / NT);
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  const int wave = (int)uniform64(tid >> 6);
   const int heads = w.q.heads, group = w.H / heads, nv = w.dv / VT;
   const int64_t chunk = blockIdx.x / heads;
   const int hk = (int)uniform64(blockIdx.x % heads);
@@ -116,23 +107,24 @@ __global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) dq[ct] = dk[ct] = zero4();
   {
-    const Operand<T> x(half ? w.k : w.q, w, hk * group, DK, 0);
-    Stage<T, DK> a;
-    a.load(x.rows(t0, have), x.step, false, tid);
-    a.store(smem + (half ? Lds::K : Lds::Q), tid);
+    const Operand<T> q(w.q, w, hk * group, DK, 0), k(w.k, w, hk * group, DK, 0);
+    Stage<T, DK> a, b;
+    a.load(q.rows(t0, have), q.step, false, tid);
+    b.load(k.rows(t0, have), k.step, false, tid);
+    a.store(smem + Lds::Q, tid);
+    b.store(smem + Lds::K, tid);
   }
   const uint32_t rb = row_base<T, VT, false>(lane);
   auto rows = [&](Frag<T>& fr, int tile, int block, int s) {
     row_frag<T>(fr, smem + tile, rows_at<T, VT, false>(rb, 16 * block), s);
   };
   auto cols = [&](Frag<T>& fr, int tile, int ct, int s) {
-    grad_col_frag<T, DK>(fr, smem + tile, 16 * (half * CT + ct), s, lane);
+    grad_col_frag<T, DK>(fr, smem + tile, 16 * ct, s, lane);
   };
   for (int x = 0; x < group; ++x) {
     const int h = hk * group + x;
     ch.h = h;
     const size_t at = ((size_t)chunk * w.H + h) * nv * (VT * DK);
-    // half of the threads fetch the rows, half the states
     Stage<T, VT> rd, ry, ru;
     Stage<T, DK> rs;
     auto fetch_rows = [&](int vt) {
@@ -148,10 +140,8 @@ __global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp
     auto fetch_state = [&](const void* p, int vt) {
       rs.load(Rows((const T*)p + at + vt * (VT * DK), VT * DK * sizeof(T)), DK * sizeof(T), false, tid);
     };
-    if (half) fetch_state(f.kept, 0);
-    else fetch_rows(0);
     __syncthreads();  // the head before is done with the decays
-    if (half == 0) {
+    {
       if (wave == 0) chunk_decays(dec, row_decay<false>(w, ch, c, lane), lane);
       if (wave == 1) {  // of the reversed chunk: its row is the decay from a token to the chunk's end and over the next
         const int64_t t = t0 + C - lane;
@@ -161,9 +151,8 @@ __global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp
         const int64_t t = t0 + lane;
         beta[lane] = t < ch.hi ? Elem<T>::load(f.beta, (size_t)t * w.H + h) : 0.f;
       }
-    } else if (wave == 3) {
-      const int64_t t = t0 + lane;
-      if (t < ch.hi) {
+      if (wave == 3 && t0 + lane < ch.hi) {
+        const int64_t t = t0 + lane;
         float d = 0.f;
         for (int vt = 0; vt < nv; ++vt) d += gp.a.dots2[((size_t)vt * w.H + h) * gp.rows + t];
         Elem<T>::store(gp.a.dbeta, (size_t)t * w.H + h, d);
@@ -178,16 +167,13 @@ __global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp
     for (int B = 0; B < 4; ++B) ee[B] = ff[B] = zero4();
     for (int vt = 0; vt < nv; ++vt) {
       if (vt > 0) __syncthreads();
-      if (half) {
-        rs.store(smem + Lds::S, tid);
-        fetch_state(gp.a.kept_r, vt);
-      } else {
-        scale_stage<T, VT>(ru, beta, tid);
-        rd.store(smem + Lds::DO, tid);
-        ry.store(smem + Lds::Y, tid);
-        ru.store(smem + Lds::U, tid);
-        if (vt + 1 < nv) fetch_rows(vt + 1);
-      }
+      fetch_rows(vt);
+      fetch_state(f.kept, vt);
+      scale_stage<T, VT>(ru, beta, tid);
+      rd.store(smem + Lds::DO, tid);
+      ry.store(smem + Lds::Y, tid);
+      ru.store(smem + Lds::U, tid);
+      rs.store(smem + Lds::S, tid);
       __syncthreads();
       Frag<T> fo[2], fy[2], fu[2];
 #pragma unroll
@@ -236,10 +222,8 @@ __global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp
         mma(fd, fy[s], fu[s]);
       }
       __syncthreads();
-      if (half) {
-        rs.store(smem + Lds::S, tid);
-        if (vt + 1 < nv) fetch_state(f.kept, vt + 1);
-      }
+      fetch_state(gp.a.kept_r, vt);
+      rs.store(smem + Lds::S, tid);
       __syncthreads();
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
@@ -297,7 +281,7 @@ __global__ __launch_bounds__(2 * NT, 2) void gdr_grad_kernel(const GradParams gp
   const Rows bq((char*)gp.a.dq + to, have * step), bk((char*)gp.a.dk + to, have * step);
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    const uint32_t off = (16 * wave + n) * step + (16 * (half * CT + ct) + 4 * g) * sizeof(T);
+    const uint32_t off = (16 * wave + n) * step + (16 * ct + 4 * g) * sizeof(T);
     if constexpr (sizeof(T) == 2) {
       bq.store8(off, u32x2_t{pack_bf16x2(dq[ct][0], dq[ct][1]), pack_bf16x2(dq[ct][2], dq[ct][3])});
       bk.store8(off, u32x2_t{pack_bf16x2(dk[ct][0], dk[ct][1]), pack_bf16x2(dk[ct][2], dk[ct][3])});
@@ -317,13 +301,13 @@ hipError_t grad(const GdrGrad& a) {
   gp.rows = w.cs ? w.T : (int64_t)w.n * w.T;
   const int64_t blocks = gp.chunks * w.q.heads;
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0xFFFFFFFFll / (2 * NT)) return hipErrorInvalidValue;
+  if (blocks > 0xFFFFFFFFll / NT) return hipErrorInvalidValue;
   constexpr int lds = GradLds<T, DK>::BYTES;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute((const void*)gdr_grad_kernel<T, DK>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((gdr_grad_kernel<T, DK>), dim3((unsigned)blocks), dim3(2 * NT), lds, (hipStream_t)w.stream, gp);
+  hipLaunchKernelGGL((gdr_grad_kernel<T, DK>), dim3((unsigned)blocks), dim3(NT), lds, (hipStream_t)w.stream, gp);
   return hipGetLastError();
 }
 

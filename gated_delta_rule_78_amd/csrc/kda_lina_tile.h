@@ -163,6 +163,8 @@ struct Rows {
   __device__ __forceinline__ u32x2_t load8(uint32_t off) const {
     return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
   }
+  __device__ __forceinline__ uint32_t load4(uint32_t off) const { return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
+  __device__ __forceinline__ uint32_t load2(uint32_t off) const { return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0); }
   __device__ __forceinline__ void store16(uint32_t off, u32x4_t x) const {
     __builtin_amdgcn_raw_buffer_store_b128(x, r, off, 0, 0);
   }
@@ -173,6 +175,8 @@ struct Rows {
   __device__ Rows(const void*, uint32_t) {}
   __device__ u32x4_t load16(uint32_t) const { return u32x4_t{}; }
   __device__ u32x2_t load8(uint32_t) const { return u32x2_t{}; }
+  __device__ uint32_t load4(uint32_t) const { return 0; }
+  __device__ uint32_t load2(uint32_t) const { return 0; }
   __device__ void store16(uint32_t, u32x4_t) const {}
   __device__ void store8(uint32_t, u32x2_t) const {}
 #endif
@@ -459,9 +463,9 @@ __device__ __forceinline__ uint32_t row_off(bool rev, int r, uint32_t step) { re
 __device__ __forceinline__ uint32_t rows_off(bool rev, int rows, uint32_t step) { return (rev ? -rows : rows) * step; }
 
 // A thread's share of one chunk's tiles, on its way from memory to LDS (NT threads).
-template <typename T, int D, bool LEAN = false>
+template <typename T, int D, bool LEAN = false, typename TILE = Tile<T, D>>
 struct Stage {
-  static constexpr int RU = Tile<T, D>::RB / 16;  // 16-byte units of a row
+  static constexpr int RU = TILE::RB / 16;  // 16-byte units of a row
   static constexpr int N = C * RU / NT;
   static constexpr int ROWS = NT / RU;            // rows at a time, a multiple of 16 for bf16
   u32x4_t r[N];
@@ -471,11 +475,11 @@ struct Stage {
     for (int i = 0; i < N; ++i) r[i] = b.load16(o + rows_off(rev, ROWS * i, step));
   }
   __device__ __forceinline__ void store(char* t, int tid) const {
-    const uint32_t o = fresh<LEAN>(Tile<T, D>::unit(tid / RU, tid % RU));
+    const uint32_t o = fresh<LEAN>(TILE::unit(tid / RU, tid % RU));
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      *(u32x4_t*)(t + (ROWS % 16 == 0 ? o + ROWS * i * Tile<T, D>::RB
-                                      : Tile<T, D>::unit(tid / RU + ROWS * i, tid % RU))) = r[i];
+      *(u32x4_t*)(t + (ROWS % 16 == 0 ? o + ROWS * i * TILE::RB
+                                      : TILE::unit(tid / RU + ROWS * i, tid % RU))) = r[i];
   }
 };
 

@@ -135,12 +135,12 @@ def test_workspaces(L):
 @pytest.mark.parametrize("dtype", [0, 1])
 @pytest.mark.parametrize("T,n", [(131072, 1024), (131072, 16384), (5000, 5000), (0, 4096)])
 def test_packed_workspaces(L, T, n, dtype):
-    """A further sequence takes at most one chunk's triangles (and in the backward its two states), a list entry
+    """A further sequence takes at most one chunk's triangles and decays (and in the backward its two states), a list entry
     and its decay gradient's sums; no state of segments."""
     H, d, es = 32, 128, (2, 4)[dtype]
     sh = ctypes.byref(kda.Shape(1, T, H, d, d, 64, dtype))
     chunks, state = T // 64 + n, H * d * d * 4
-    tri = chunks * H * 2560
+    tri = chunks * H * (2560 + 98)  # two triangles, and decays and strengths, in pairs of fp32
     ends = T // (64 * 8) * state
     assert L.kda_gdr_chunk_fwd_varlen_workspace_size(sh, n) <= tri * 8 + 3 * ends + 32 * n + T + 65536
     rows = T * H * (d * es + 3 * 4 * (d // 64))
