@@ -340,7 +340,7 @@ static_assert(sizeof(TokenLds) == kTokenFloats * 4, "as in memory");
 // three bf16 terms (all 24 bits): S against k, N and what it multiplies, b o r against k.  The forward's
 // outputs, which are rounded to bf16 themselves, take S, P and b o r in two (16 bits).
 template <typename T, int DK, int MODE>
-__global__ __launch_bounds__(2 * NT) void gdr_walk_kernel(const GdrParams gp) {
+__global__ __launch_bounds__(2 * NT, 2) void gdr_walk_kernel(const GdrParams gp) {
   typedef WalkLds<T, DK, MODE> Lds;
   constexpr bool REV = is_rev(MODE), SEG = is_seg(MODE);
   constexpr bool HAS_Q = MODE != kSegFwd, HAS_P = HAS_Q, OUT = MODE == kFwd || MODE == kTrain, DOTS = MODE == kTrain || MODE == kRev;
@@ -703,7 +703,7 @@ __global__ __launch_bounds__(NT) void gdr_link_kernel(const GdrParams gp, bool r
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, n = lane & 15;
   Chain ch;
   if (!ch.place(gp.p, rev, blockIdx.x)) return;
-  if (!ch.tail || ch.nsg == 1) return;  // one workgroup for each chain
+  if (ch.sg != 0 || ch.nsg == 1) return;  // one workgroup for each chain
   f32x4_t S[CT];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) S[ct] = zero4();
@@ -778,9 +778,19 @@ hipError_t prep(const GdrParams& gp) {
   return gp.p.w.rev ? prep<T, DK, true>(gp) : prep<T, DK, false>(gp);
 }
 
+// Slots of a packed batch's list that segments before another one can have: they are L chunks long, and the list has
+// those first.
+int64_t cut_slots(const WalkParams& p) {
+  const LinaWalk& w = p.w;
+  return w.cs ? std::min(p.nseg, (int64_t)w.T / ((int64_t)C * (w.L - 1) + 1)) : p.nseg;
+}
+
 template <typename T, int DK, int MODE>
 hipError_t walk(GdrParams gp) {
-  if constexpr (is_seg(MODE)) gp.p.nv += DK / VT;
+  if constexpr (is_seg(MODE)) {
+    gp.p.nv += DK / VT;
+    gp.p.nseg = cut_slots(gp.p);
+  }
   return launch(gdr_walk_kernel<T, DK, MODE>, walk_blocks(gp.p), 2 * NT, WalkLds<T, DK, MODE>::BYTES, gp.p.w.stream, gp);
 }
 template <typename T, int DK>
@@ -792,7 +802,9 @@ template <typename T, int DK>
 hipError_t segments(const GdrParams& gp) {
   const hipError_t e = gp.p.w.rev ? walk<T, DK, kSegRev>(gp) : walk<T, DK, kSegFwd>(gp);
   if (e != hipSuccess) return e;
-  return launch(gdr_link_kernel<DK>, walk_blocks(gp.p), NT, DK * (DK + 4) * 4, gp.p.w.stream, gp, gp.p.w.rev);
+  GdrParams link = gp;
+  link.p.nseg = cut_slots(gp.p);
+  return launch(gdr_link_kernel<DK>, walk_blocks(link.p), NT, DK * (DK + 4) * 4, gp.p.w.stream, link, gp.p.w.rev);
 }
 
 template <typename F>

@@ -15,6 +15,8 @@ struct VerifyArgs {
   const float *u, *u_next;
   int *accepted, *next;  // [B]
   double* sums;          // [B][tiles][2]
+  int* rows;             // [B][2]: drafts that stand, and the one that does not
+  int groups;            // workgroups of a sequence
   bool bf16;
   void* stream;
 };

@@ -6,7 +6,9 @@
 // sum passes u_next times the whole.  All of it in fp64, so that the index does not hang on the order of a sum.
 //
 // Only row n of p and q is read whole, in tiles of 2,048 tokens: the first kernel sums each tile (weights, and p's
-// own, for where the weights are all zero), the second finds the tile and the token in it.
+// own, for where the weights are all zero), the second finds the tile and the token in it.  What both wait for is one
+// access to memory after another: the drafts, their probabilities, the row; so a workgroup of the first goes through several
+// tiles of a row once it knows which.
 #include <math.h>
 
 #include "kda_common.h"
@@ -59,57 +61,73 @@ __device__ __forceinline__ Row find_row(const VerifyArgs& a, int64_t b) {
       break;
     }
   }
-  r.p = ((size_t)b * (a.K + 1) + r.n) * a.V;
-  r.q = ((size_t)b * a.K + min(r.n, max(a.K - 1, 0))) * a.V;
   return r;
 }
 
-// the two weights of token j: after a refusal, and the target's own
-template <typename T>
-__device__ __forceinline__ void weights(const VerifyArgs& a, const Row& r, int j, double& rest, double& own) {
-  own = weight(Elem<T>::load(a.p, r.p + j));
+__device__ __forceinline__ void place_row(const VerifyArgs& a, int64_t b, Row& r) {
+  r.p = ((size_t)b * (a.K + 1) + r.n) * a.V;
+  r.q = ((size_t)b * a.K + min(r.n, max(a.K - 1, 0))) * a.V;
+}
+
+// the two weights of token j with probabilities p and q: after a refusal, and the target's own
+__device__ __forceinline__ void weights(const VerifyArgs& a, const Row& r, int j, float p, float q, double& rest, double& own) {
+  own = weight(p);
   rest = own;
   if (r.refused >= 0) {
-    const double less = a.q ? weight(Elem<T>::load(a.q, r.q + j)) : j == r.refused ? 1. : 0.;
+    const double less = a.q ? weight(q) : j == r.refused ? 1. : 0.;
     rest = own > less ? own - less : 0.;
   }
 }
 
 template <typename T>
 __global__ __launch_bounds__(NT) void verify_sum_kernel(const VerifyArgs a) {
-  __shared__ double part[2][NT / 64];
+  __shared__ double part[2][2][NT / 64];
   const int tid = threadIdx.x;
-  const int64_t b = blockIdx.x / a.tiles;
-  const int tile = (int)(blockIdx.x % a.tiles);
-  const Row r = find_row<T>(a, b);
-  double rest = 0., own = 0.;
+  const int64_t b = blockIdx.x / a.groups;
+  const int first = (int)(blockIdx.x % a.groups);
+  Row r = find_row<T>(a, b);
+  place_row(a, b, r);
+  if (first == 0 && tid == 0) {
+    a.rows[2 * b] = r.n;
+    a.rows[2 * b + 1] = r.refused;
+  }
+  const bool both = a.q && r.refused >= 0;
+  float p[PER], q[PER];
+  auto fetch = [&](int tile) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int j = tile * kVerifyTile + i * NT + tid;
-    double x = 0., y = 0.;
-    if (j < a.V) weights<T>(a, r, j, x, y);
-    rest += x;
-    own += y;
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    rest += __shfl_xor(rest, off);
-    own += __shfl_xor(own, off);
-  }
-  if ((tid & 63) == 0) {
-    part[0][tid >> 6] = rest;
-    part[1][tid >> 6] = own;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    double x = 0., y = 0.;
-    for (int i = 0; i < NT / 64; ++i) {
-      x += part[0][i];
-      y += part[1][i];
+    for (int i = 0; i < PER; ++i) {
+      const int64_t j = (int64_t)tile * kVerifyTile + i * NT + tid;
+      p[i] = j < a.V ? Elem<T>::load(a.p, r.p + j) : 0.f;
+      q[i] = both && j < a.V ? Elem<T>::load(a.q, r.q + j) : 0.f;
     }
-    double* to = a.sums + ((size_t)b * a.tiles + tile) * 2;
-    to[0] = x;
-    to[1] = y;
+  };
+  fetch(first);
+  int par = 0;
+  for (int tile = first; tile < a.tiles; tile += a.groups, par ^= 1) {
+    double rest = 0., own = 0.;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      double x, y;
+      weights(a, r, tile * kVerifyTile + i * NT + tid, p[i], q[i], x, y);
+      rest += x;
+      own += y;
+    }
+    if (tile + a.groups < a.tiles) fetch(tile + a.groups);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      rest += __shfl_xor(rest, off);
+      own += __shfl_xor(own, off);
+    }
+    if ((tid & 63) == 0) {
+      part[par][0][tid >> 6] = rest;
+      part[par][1][tid >> 6] = own;
+    }
+    __syncthreads();  // two buffers: one barrier a tile
+    if (tid < 2) {
+      double x = 0.;
+      for (int i = 0; i < NT / 64; ++i) x += part[par][tid][i];
+      a.sums[((size_t)b * a.tiles + tile) * 2 + tid] = x;
+    }
   }
 }
 
@@ -119,7 +137,10 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(const VerifyArgs a) {
   __shared__ int found, last;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t b = blockIdx.x;
-  const Row r = find_row<T>(a, b);
+  Row r;
+  r.n = a.rows[2 * b];
+  r.refused = a.rows[2 * b + 1];
+  place_row(a, b, r);
   const double* sums = a.sums + (size_t)b * a.tiles * 2;
   if (tid == 0) {
     found = 0x7FFFFFFF;
@@ -178,7 +199,8 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(const VerifyArgs a) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     double x = 0., y = 0.;
-    if (j0 + i < a.V) weights<T>(a, r, j0 + i, x, y);
+    if (j0 + i < a.V)
+      weights(a, r, j0 + i, Elem<T>::load(a.p, r.p + j0 + i), a.q && r.refused >= 0 ? Elem<T>::load(a.q, r.q + j0 + i) : 0.f, x, y);
     w[i] = rest ? x : y;
     sum += w[i];
   }
@@ -209,7 +231,7 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(const VerifyArgs a) {
 
 template <typename T>
 hipError_t verify(const VerifyArgs& a) {
-  const int64_t blocks = (int64_t)a.B * a.tiles;
+  const int64_t blocks = (int64_t)a.B * a.groups;
   if (blocks > 0xFFFFFFFFll / NT) return hipErrorInvalidValue;
   hipLaunchKernelGGL(verify_sum_kernel<T>, dim3((unsigned)blocks), dim3(NT), 0, (hipStream_t)a.stream, a);
   const hipError_t e = hipGetLastError();

@@ -21,7 +21,7 @@ extern "C" {
 
 size_t kda_verify_drafts_workspace_size(int B, int K, int V, int dtype) {
   if (check_sizes(B, K, V, dtype) != KDA_OK) return 0;
-  return (size_t)B * ((V + (size_t)kda::kVerifyTile - 1) / kda::kVerifyTile) * 16;
+  return (size_t)B * (((V + (size_t)kda::kVerifyTile - 1) / kda::kVerifyTile) * 16 + 8);
 }
 
 int kda_verify_drafts(int B, int K, int V, int dtype, const void* target_probs, const int* drafts,
@@ -48,9 +48,12 @@ int kda_verify_drafts(int B, int K, int V, int dtype, const void* target_probs, 
     for (int j = i + 1; j < 3; ++j)
       if (overlap(out[i], out[j])) return KDA_ERR_ALIAS;
   }
-  const kda::VerifyArgs a{B,      K,        V,          (int)((V + (int64_t)kda::kVerifyTile - 1) / kda::kVerifyTile),
-                          target_probs, draft_probs, drafts, u, u_next, accepted, next_token, (double*)workspace,
-                          dtype == KDA_BF16, stream};
+  const int tiles = (int)((V + (int64_t)kda::kVerifyTile - 1) / kda::kVerifyTile);
+  double* sums = (double*)workspace;
+  // eight workgroups to a compute unit, if there are so many tiles
+  const int groups = (int)(B >= 2048 ? 1 : tiles < 2048 / B ? tiles : 2048 / B);
+  const kda::VerifyArgs a{B,        K,          V,    tiles, target_probs, draft_probs,       drafts, u, u_next,
+                          accepted, next_token, sums, (int*)(sums + (size_t)B * tiles * 2), groups, dtype == KDA_BF16, stream};
   return kda::launch_verify(a) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
