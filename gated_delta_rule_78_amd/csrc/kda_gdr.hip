@@ -778,8 +778,8 @@ hipError_t prep(const GdrParams& gp) {
   return gp.p.w.rev ? prep<T, DK, true>(gp) : prep<T, DK, false>(gp);
 }
 
-// Slots of a packed batch's list that segments before another one can have: they are L chunks long, and the list has
-// those first.
+// Slots of a packed batch's list that a sequence's segments but its last can have: they are L chunks long, and the list has
+// those first.  (In reverse it is the first one that no other starts from: the last, of any length, is walked too.)
 int64_t cut_slots(const WalkParams& p) {
   const LinaWalk& w = p.w;
   return w.cs ? std::min(p.nseg, (int64_t)w.T / ((int64_t)C * (w.L - 1) + 1)) : p.nseg;
@@ -789,7 +789,7 @@ template <typename T, int DK, int MODE>
 hipError_t walk(GdrParams gp) {
   if constexpr (is_seg(MODE)) {
     gp.p.nv += DK / VT;
-    gp.p.nseg = cut_slots(gp.p);
+    if (!is_rev(MODE)) gp.p.nseg = cut_slots(gp.p);
   }
   return launch(gdr_walk_kernel<T, DK, MODE>, walk_blocks(gp.p), 2 * NT, WalkLds<T, DK, MODE>::BYTES, gp.p.w.stream, gp);
 }

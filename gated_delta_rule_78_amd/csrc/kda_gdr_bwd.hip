@@ -1,6 +1,6 @@
 // kda_gdr_bwd.hip -- gradients of q, k and beta of the gated delta rule with one decay per head, chunk by
 // chunk, from what the two walks left: S, the state a chunk starts from, R, the gradient of the state behind
-// it, r = v - e^g S^T k, y = dv.  With u = b o r and the chunk's decays e^G (from its start), e^G' (to its end, the
+// it, r = v - e^g S^T k, y = dv.  With u = b o r (b is taken to the products, fp32) and the chunk's decays e^G (from its start), e^G' (to its end, the
 // next token's decay included), D_ij = e^{G_i - G_j},
 //   E_ij = D_ij do_i . u_j (j <= i),   F_ij = D_ij y_i . u_j (j < i),
 //   dq = E K + e^G o (do S^T),
@@ -47,30 +47,13 @@ __device__ __forceinline__ void grad_col_frag(Frag<T>& f, const char* t, int c0,
   }
 }
 
-// a staged tile's elements times their row's factor
-template <typename T, int D>
-__device__ __forceinline__ void scale_stage(Stage<T, D>& r, const float* by, int tid) {
-  typedef Stage<T, D> St;
-#pragma unroll
-  for (int i = 0; i < St::N; ++i) {
-    const float f = by[tid / St::RU + St::ROWS * i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 2)
-        r.r[i][j] = pack_bf16x2(__uint_as_float(r.r[i][j] << 16) * f, __uint_as_float(r.r[i][j] & 0xFFFF0000u) * f);
-      else
-        r.r[i][j] = __float_as_uint(__uint_as_float(r.r[i][j]) * f);
-    }
-  }
-}
-
 template <typename T, int DK>
 __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void gdr_grad_kernel(const GradParams gp) {
   typedef GradLds<T, DK> Lds;
   constexpr int CT = DK / 16;
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) Decays dec, back;
-  __shared__ float beta[C];
+  __shared__ __align__(16) float beta[C];
   const GdrWalk& f = gp.a.f;
   const LinaWalk& w = f.walk;
   // The wave's number in a scalar: branches on it are jumps.  Under an execution mask, as the compiler may
@@ -159,7 +142,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void gdr_grad_kernel(co
       }
     }
     __syncthreads();
-    const float row = dec.row[16 * wave + n], end = back.row[C - 1 - 16 * wave - n];
+    const float bn = beta[16 * wave + n], row = dec.row[16 * wave + n], end = back.row[C - 1 - 16 * wave - n] * bn;
     // scores of own tokens (columns) with block B's (rows): E, as dq and dk take it before and behind the own
     // block, and F + F^T; of the own block both halves
     f32x4_t ee[4], ff[4], ed = zero4(), fd = zero4();
@@ -169,7 +152,6 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void gdr_grad_kernel(co
       if (vt > 0) __syncthreads();
       fetch_rows(vt);
       fetch_state(f.kept, vt);
-      scale_stage<T, VT>(ru, beta, tid);
       rd.store(smem + Lds::DO, tid);
       ry.store(smem + Lds::Y, tid);
       ru.store(smem + Lds::U, tid);
@@ -246,22 +228,25 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void gdr_grad_kernel(co
     for (int B = 0; B < 4; ++B) {
       const float4 jh4 = *(const float4*)&dec.hi[16 * B + 4 * g], jl4 = *(const float4*)&dec.lo[16 * B + 4 * g];
       const float jh[4] = {jh4.x, jh4.y, jh4.z, jh4.w}, jl[4] = {jl4.x, jl4.y, jl4.z, jl4.w};
+      const float4 b4 = *(const float4*)&beta[16 * B + 4 * g];
+      const float bj[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float d = (ih - jh[i]) + (il - jl[i]);  // exponent from token 16 B + 4 g + i to the own one
         const int j = 16 * B + 4 * g + i - 16 * wave;
-        const float r = fast_exp2(j <= n ? d : -d);
+        const float r = fast_exp2(j <= n ? d : -d) * (j <= n ? bj[i] : bn);  // b of the token whose r it is
         e1[B][i] = j <= n ? ee[B][i] * r : 0.f;
         e2[B][i] = j >= n ? (B == wave ? ed[i] : ee[B][i]) * r : 0.f;
         ff[B][i] = j < n ? -ff[B][i] * r : j > n ? -(B == wave ? fd[i] : ff[B][i]) * r : 0.f;
       }
     }
-    Frag<T> f1[2], f2[2], f3[2];
+    Terms<T, kMost<T>> f1[2], f2[2], f3[2];
+    const Residual res;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      f1[s].from_acc(e1[2 * s], e1[2 * s + 1]);
-      f2[s].from_acc(e2[2 * s], e2[2 * s + 1]);
-      f3[s].from_acc(ff[2 * s], ff[2 * s + 1]);
+      split(res, e1[2 * s], e1[2 * s + 1], f1[s]);
+      split(res, e2[2 * s], e2[2 * s + 1], f2[s]);
+      split(res, ff[2 * s], ff[2 * s + 1], f3[s]);
     }
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -269,10 +254,14 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void gdr_grad_kernel(co
       for (int s = 0; s < 2; ++s) {
         Frag<T> a;
         cols(a, Lds::K, ct, s);
-        mma(dq[ct], a, f1[s]);
-        mma(dk[ct], a, f3[s]);
+#pragma unroll
+        for (int m = 0; m < kMost<T>; ++m) {
+          mma(dq[ct], a, f1[s].f[m]);
+          mma(dk[ct], a, f3[s].f[m]);
+        }
         cols(a, Lds::Q, ct, s);
-        mma(dk[ct], a, f2[s]);
+#pragma unroll
+        for (int m = 0; m < kMost<T>; ++m) mma(dk[ct], a, f2[s].f[m]);
         in_turn();
       }
   }
