@@ -163,8 +163,6 @@ struct Rows {
   __device__ __forceinline__ u32x2_t load8(uint32_t off) const {
     return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
   }
-  __device__ __forceinline__ uint32_t load4(uint32_t off) const { return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
-  __device__ __forceinline__ uint32_t load2(uint32_t off) const { return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0); }
   __device__ __forceinline__ void store16(uint32_t off, u32x4_t x) const {
     __builtin_amdgcn_raw_buffer_store_b128(x, r, off, 0, 0);
   }
@@ -175,8 +173,6 @@ struct Rows {
   __device__ Rows(const void*, uint32_t) {}
   __device__ u32x4_t load16(uint32_t) const { return u32x4_t{}; }
   __device__ u32x2_t load8(uint32_t) const { return u32x2_t{}; }
-  __device__ uint32_t load4(uint32_t) const { return 0; }
-  __device__ uint32_t load2(uint32_t) const { return 0; }
   __device__ void store16(uint32_t, u32x4_t) const {}
   __device__ void store8(uint32_t, u32x2_t) const {}
 #endif
