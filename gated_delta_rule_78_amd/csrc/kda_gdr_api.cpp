@@ -46,7 +46,9 @@ int segment_override() {
 // A chain (sequence, head, 64 value columns) is walked in order.  With few chains it is cut into segments,
 // which costs a first pass over all but the last (the value columns and the transfer's, about 0.7 of a
 // step each) and the links between them (about 1.5 steps each, one after another); a cut is taken where this sum of steps on
-// 256 compute units is least.  Packed chains are cut, or not, where their lengths are known
+// 256 compute units is least.  As it chooses, whole and in segments of 16 chunks: 131,072 tokens, 16 heads 2,205, 5,698 and
+// 3,602 us; 8,192 tokens, 16 heads 206, 370 and 206; 2 x 8,192, 32 heads 429, 431 (whole) and 607; 2,048 tokens, 8 heads 103,
+// 108 and 113.  Packed chains are cut, or not, where their lengths are known
 // (lina_offsets_kernel); L is then the least that their segments may have, a compute unit's share of all steps.
 Plan gdr_plan(const kda_shape& s, int n_seqs) {
   const bool packed = n_seqs >= 0;
@@ -129,7 +131,9 @@ int start(kda::GdrWalk& a, const kda_shape& s, const Layout& l, int n_seqs, cons
   if (n_seqs < 0) return KDA_OK;
   w.cs = (const int*)(ws + l.off_cs);
   w.list = (const int*)(ws + l.off_list);
-  // cut chains take three times the steps
+  // cut chains take three times the steps, so chains of up to 3 shares are walked whole: 20,011 tokens in 24 sequences, 8 heads,
+  // the longest 0.15 of them (2.2 shares) 168 us whole, 174 cut, 0.3 (4.5 shares) 292 and 181; 32 heads, one of half (1.8 shares)
+  // 523 and 537
   return kda::launch_lina_offsets(cu, n_seqs, s.T, w.L, s.H * (s.dv / 64), (int*)(ws + l.off_cs),
                                   (int*)(ws + l.off_list), stream, 85) == hipSuccess
              ? KDA_OK

@@ -8,7 +8,8 @@
 // Only row n of p and q is read whole, in tiles of 2,048 tokens: the first kernel sums each tile (weights, and p's
 // own, for where the weights are all zero), the second finds the tile and the token in it.  What both wait for is one
 // access to memory after another: the drafts, their probabilities, the row; so a workgroup of the first goes through several
-// tiles of a row once it knows which.
+// tiles of a row once it knows which.  128 sequences over 131,072 tokens, fp32 (134 MB of p and q where a draft is refused):
+// 31 us, 4.4 TB/s, and 9 for the second kernel; a single sequence 5 and 9, latency.  Tiles of 4,096 tokens were slower.
 #include <math.h>
 
 #include "kda_common.h"

@@ -50,7 +50,8 @@ int kda_verify_drafts(int B, int K, int V, int dtype, const void* target_probs, 
   }
   const int tiles = (int)((V + (int64_t)kda::kVerifyTile - 1) / kda::kVerifyTile);
   double* sums = (double*)workspace;
-  // eight workgroups to a compute unit, if there are so many tiles
+  // eight workgroups to a compute unit, if there are so many tiles: 128 rows of 131,072 tokens 33.8 us, two to a unit 38.7, one
+  // for each tile 36.7; 512 rows of 32,000 35.5, 40.7 and 38.7; a single row 14.1, 15.1 and 15.0
   const int groups = (int)(B >= 2048 ? 1 : tiles < 2048 / B ? tiles : 2048 / B);
   const kda::VerifyArgs a{B,        K,          V,    tiles, target_probs, draft_probs,       drafts, u, u_next,
                           accepted, next_token, sums, (int*)(sums + (size_t)B * tiles * 2), groups, dtype == KDA_BF16, stream};
