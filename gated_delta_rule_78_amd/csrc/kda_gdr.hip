@@ -344,9 +344,9 @@ static_assert(sizeof(TokenLds) == kTokenFloats * 4, "as in memory");
 //
 // What bounds it: the chain from S through K S, r and b o r back to S.  A step of the forward (d = 128, bf16) has 182 products
 // a wave and takes 6,400 to 6,700 cycles, matrix units 35 to 38% busy; conflict-free tiles, another order and other ways to
-// split changed it by a few percent.  B4 H32 T8K: 395 us for 128 steps in a row; in training 629 forward, 800 in reverse, where
+// split changed it by a few percent.  B4 H32 T8K: 409 us for 128 steps in a row; in training 629 forward, 800 in reverse, where
 // states and r are written too and the products of Q and d_o come on top.  Of 131,072 tokens, 16 heads (32 chains): end states
-// and transfers of segments 1,075 us, links 63, outputs 770.  Two workgroups to a compute unit in the first pass (128
+// and transfers of segments 1,075 us, links 63, outputs 779.  Two workgroups to a compute unit in the first pass (128
 // registers) spill: 4,260 us for the whole call instead of 2,227.
 template <typename T, int DK, int MODE>
 __global__ __launch_bounds__(2 * NT, 2) void gdr_walk_kernel(const GdrParams gp) {

@@ -548,9 +548,9 @@ int kda_gdr_chunk_fwd_varlen(const kda_shape* shape, int qk_heads, const int* cu
  *   d_o                 : [B, T, H, dv], dtype of q;  d_final_state : fp32 or NULL (zeros)
  *   dq, dk, dv, d_beta  : outputs in the layout and dtype of q, k, v, beta (sums are fp32; q / k
  *                         heads that serve several heads get the sum over them, rounded once).
- *                         With bf16 inputs dq and dk take the states of both directions, dv,
- *                         beta (v - e^g S^T k) and the scores rounded to bf16, d_beta the second
- *                         of the vectors that it is the product of.
+ *                         With bf16 inputs dq and dk take the states of both directions, dv and
+ *                         v - e^g S^T k rounded to bf16 and the scores in 16 bits, d_beta takes
+ *                         v - e^g S^T k so too.
  *   d_log_decay         : fp32 [B, T, H], or NULL when not wanted.  0 where e^g is under 2^-126,
  *                         -inf among them.
  *   d_initial_state     : fp32, or NULL when not wanted
