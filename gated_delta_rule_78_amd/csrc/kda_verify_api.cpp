@@ -10,9 +10,12 @@ namespace {
 
 int check_sizes(int B, int K, int V, int dtype) {
   if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_DTYPE;
-  if (B < 0 || K < 0 || V < 1 || V > (1 << 30)) return KDA_ERR_SHAPE;
-  const int64_t tiles = (V + (int64_t)kda::kVerifyTile - 1) / kda::kVerifyTile;
-  return (int64_t)B * tiles > 0xFFFFFFFFll / 256 || (int64_t)B * (K + 1) > (int64_t(1) << 31) ? KDA_ERR_SHAPE : KDA_OK;
+  // up to 2^30 the kernels' K + 1 and their 64 drafts at a time stay in 32 bits
+  if (B < 0 || K < 0 || K > (1 << 30) || V < 1 || V > (1 << 30)) return KDA_ERR_SHAPE;
+  const int64_t tiles = (V + (int64_t)kda::kVerifyTile - 1) / kda::kVerifyTile, rows = (int64_t)B * ((int64_t)K + 1);
+  // probabilities: up to 2^59 of them, 2^61 bytes
+  return (int64_t)B * tiles > 0xFFFFFFFFll / 256 || rows > (int64_t(1) << 31) || rows > (int64_t(1) << 59) / V ? KDA_ERR_SHAPE
+                                                                                                            : KDA_OK;
 }
 
 }  // namespace

@@ -602,8 +602,8 @@ int kda_gdr_decode_tokens(const kda_shape* shape, int qk_heads, const int* count
  *   workspace    : the size below, 8-byte aligned
  * Entries that are negative or not finite weigh nothing (a NaN never lets a draft stand).  Weights that are
  * all zero after a refusal give way to p_n; next_token is -1 where that weighs nothing either.
- * Alignment: the elements'.  No output may overlap an input, another output or the workspace.  V <= 2^30;
- * more than 2^24 pieces of 2,048 tokens are KDA_ERR_SHAPE.
+ * Alignment: the elements'.  No output may overlap an input, another output or the workspace.  K or V over
+ * 2^30, more than 2^31 rows of p, 2^59 probabilities or 2^24 pieces of 2,048 tokens are KDA_ERR_SHAPE.
  */
 size_t kda_verify_drafts_workspace_size(int B, int K, int V, int dtype); /* 0 if invalid */
 int kda_verify_drafts(int B, int K, int V, int dtype, const void* target_probs, const int* drafts,

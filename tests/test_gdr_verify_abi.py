@@ -277,3 +277,15 @@ def test_verified_tokens_are_distributed_as_the_target():
             tokens = np.bincount([one(ul) for ul in grid], minlength=V) / n
             got += q[x] * (1 - share) * tokens
     assert np.abs(got - p[0]).max() <= 3.0 / n
+
+
+def test_verify_refuses_counts_that_pass_their_types(L):
+    """K + 1 behind 32 bits, and probabilities whose bytes pass 64."""
+    size = L.kda_verify_drafts_workspace_size
+    for B, K, V in ((1, 2 ** 31 - 1, 100), (64, 2 ** 31 - 1, 100), (1, (1 << 30) + 1, 1), (32, (1 << 26) - 1, 1 << 30),
+                    (1, 1 << 30, 1 << 30)):
+        for dtype in (0, 1):
+            assert size(B, K, V, dtype) == 0 and _ver(L, B=B, K=K, V=V, dtype=dtype) == SHAPE, (B, K, V)
+    # the largest that are left, up to the workspace's check
+    assert size(1, 1 << 30, 100, 1) > 0 and _ver(L, B=1, K=1 << 30, V=100, nws=0) == WORKSPACE
+    assert size(31, (1 << 24) - 1, 1 << 30, 0) > 0
