@@ -28,9 +28,7 @@ int check_shape(const kda_shape* s, bool decode, int* es) {
   if (!s) return KDA_ERR_NULL;
   if (s->dtype != KDA_BF16 && s->dtype != KDA_F32) return KDA_ERR_DTYPE;
   if (s->B < 0 || s->H < 1 || s->dk < 1 || s->dv < 1 || (!decode && s->T < 0)) return KDA_ERR_SHAPE;
-  const int64_t T = decode ? 1 : s->T;
-  const int64_t rows = (int64_t)s->B * T * s->H;
-  if (rows > (int64_t(1) << 40) / 256) return KDA_ERR_SHAPE;
+  if (too_many_rows(s->B, decode ? 1 : s->T, s->H)) return KDA_ERR_SHAPE;
   if (!supported_width(s->dk) || !supported_width(s->dv)) return KDA_ERR_UNSUPPORTED;
   if (!decode && s->chunk != 0 && s->chunk != 64) return KDA_ERR_UNSUPPORTED;
   *es = s->dtype == KDA_BF16 ? 2 : 4;

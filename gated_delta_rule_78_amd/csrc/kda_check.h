@@ -17,6 +17,9 @@ bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.l
 
 bool misaligned(const void* p, unsigned bytes = 16) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
+// Rows of a call: up to 2^32.  B, T >= 0, H >= 1; the product of all three may pass 64 bits.
+bool too_many_rows(int64_t B, int64_t T, int64_t H) { return B * T > (int64_t(1) << 32) / H; }
+
 bool supported_width(int d) { return d == 64 || d == 128; }
 
 }  // namespace

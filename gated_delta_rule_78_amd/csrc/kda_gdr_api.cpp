@@ -20,7 +20,7 @@ int check_gdr_shape(const kda_shape* s, int qk_heads, bool decode, int n_seqs, i
   if (s->B < 0 || s->H < 1 || s->H > 65535 || qk_heads < 1 || s->dk < 1 || s->dv < 1 || s->T < 0) return KDA_ERR_SHAPE;
   if (s->H % qk_heads != 0) return KDA_ERR_SHAPE;
   if (n_seqs >= 0 && (s->B != 1 || n_seqs > (1 << 24))) return KDA_ERR_SHAPE;
-  if ((int64_t)s->B * s->T * s->H > (int64_t(1) << 40) / 256) return KDA_ERR_SHAPE;
+  if (too_many_rows(s->B, s->T, s->H)) return KDA_ERR_SHAPE;
   if (!supported_width(s->dk) || !supported_width(s->dv)) return KDA_ERR_UNSUPPORTED;
   if (!decode && s->chunk != 0 && s->chunk != 64) return KDA_ERR_UNSUPPORTED;
   *es = s->dtype == KDA_BF16 ? 2 : 4;

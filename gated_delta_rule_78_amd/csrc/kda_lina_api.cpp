@@ -22,8 +22,7 @@ int check_lina_shape(const kda_shape* s, int qk_heads, bool decode, int n_seqs, 
     return KDA_ERR_SHAPE;
   if (s->H % qk_heads != 0) return KDA_ERR_SHAPE;
   if (n_seqs >= 0 && (s->B != 1 || n_seqs > (1 << 24))) return KDA_ERR_SHAPE;
-  const int64_t rows = (int64_t)s->B * (decode && s->T < 1 ? 1 : s->T) * s->H;
-  if (rows > (int64_t(1) << 40) / 256) return KDA_ERR_SHAPE;
+  if (too_many_rows(s->B, decode && s->T < 1 ? 1 : s->T, s->H)) return KDA_ERR_SHAPE;
   if (!supported_width(s->dk) || !supported_width(s->dv)) return KDA_ERR_UNSUPPORTED;
   if (!decode && s->chunk != 0 && s->chunk != 64) return KDA_ERR_UNSUPPORTED;
   *es = s->dtype == KDA_BF16 ? 2 : 4;

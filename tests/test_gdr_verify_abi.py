@@ -289,3 +289,15 @@ def test_verify_refuses_counts_that_pass_their_types(L):
     # the largest that are left, up to the workspace's check
     assert size(1, 1 << 30, 100, 1) > 0 and _ver(L, B=1, K=1 << 30, V=100, nws=0) == WORKSPACE
     assert size(31, (1 << 24) - 1, 1 << 30, 0) > 0
+
+
+@pytest.mark.parametrize("B,T,H", [(1 << 30, 1 << 30, 16), (1 << 30, 1 << 30, 32768), (2 ** 31 - 1, 2 ** 31 - 1, 48)])
+def test_row_counts_that_pass_64_bits(L, B, T, H):
+    """B T H beyond 64 bits (2^64, 2^75; 48 (2^31 - 1)^2) is refused like any other count of rows over 2^32."""
+    ref_ = ctypes.byref(kda.Shape(B, T, H, 64, 64, 64, 0))
+    for size in (L.kda_gdr_chunk_fwd_workspace_size, L.kda_gdr_chunk_bwd_workspace_size, L.kda_lina_chunk_fwd_workspace_size):
+        assert size(ref_) == 0
+    assert L.kda_lina_chunk_bwd_workspace_size(ref_, H) == 0
+    assert L.kda_chunk_fwd_workspace_size(ref_) == 0 and L.kda_chunk_bwd_workspace_size(ref_) == 0
+    assert _fwd(L, B=B, T=T, H=H, Hk=H) == SHAPE and _bwd(L, B=B, T=T, H=H, Hk=H) == SHAPE
+    assert _tok(L, B=B, T=T, H=H, Hk=H) == SHAPE
