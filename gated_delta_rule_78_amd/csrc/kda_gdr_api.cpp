@@ -50,6 +50,9 @@ int segment_override() {
 // 3,602 us; 8,192 tokens, 16 heads 206, 370 and 206; 2 x 8,192, 32 heads 429, 431 (whole) and 607; 2,048 tokens, 8 heads 103,
 // 108 and 113.  Packed chains are cut, or not, where their lengths are known
 // (lina_offsets_kernel); L is then the least that their segments may have, a compute unit's share of all steps.
+// What a link takes is its product's: 7.5 us at d_k = 128, 1.6 at 64, of a step (bf16 3.0 and 2.0 us, fp32 8.7 and 4.8)
+// 2.5, 0.8, 0.9 and 0.35.  1.5 is between them and suits both directions: at 3 the forward of 131,072 tokens, one head, takes
+// 577 us instead of 597, the backward 1,537 instead of 1,482.
 Plan gdr_plan(const kda_shape& s, int n_seqs) {
   const bool packed = n_seqs >= 0;
   const int nv = s.dv / 64, nk = s.dk / 64;
@@ -131,11 +134,14 @@ int start(kda::GdrWalk& a, const kda_shape& s, const Layout& l, int n_seqs, cons
   if (n_seqs < 0) return KDA_OK;
   w.cs = (const int*)(ws + l.off_cs);
   w.list = (const int*)(ws + l.off_list);
+  // A link against both walks' steps of a segment, in tenths.  One sequence of 131,072 tokens, one head, without and with it:
+  // bf16, 128 x 128 1,042 and 576 us, 128 x 64 1,809 and 574, 64 x 64 485 and 265; fp32, 32,768 tokens 620 and 502.
+  const int link = segment_override() > 0 ? 0 : s.dk == 128 ? (w.bf16 ? 12 : 5) : (w.bf16 ? 4 : 2);
   // cut chains take three times the steps, so chains of up to 3 shares are walked whole: 20,011 tokens in 24 sequences, 8 heads,
   // the longest 0.15 of them (2.2 shares) 168 us whole, 174 cut, 0.3 (4.5 shares) 292 and 181; 32 heads, one of half (1.8 shares)
   // 523 and 537
   return kda::launch_lina_offsets(cu, n_seqs, s.T, w.L, s.H * (s.dv / 64), (int*)(ws + l.off_cs),
-                                  (int*)(ws + l.off_list), stream, 85) == hipSuccess
+                                  (int*)(ws + l.off_list), stream, 85, link) == hipSuccess
              ? KDA_OK
              : KDA_ERR_HIP;
 }

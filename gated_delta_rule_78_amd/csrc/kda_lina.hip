@@ -690,8 +690,9 @@ WalkParams walk_params(const LinaWalk& w) {
 // (1.7 shares): 308 us whole, 273 cut; 0.6 of all (2.2 shares): 369 and 283; 24 like ones: 218 whole.
 constexpr int NTB = 1024;
 __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict__ cu, int nseq, int T, int least,
-                                                           int chains, int cut, int64_t slots,
-                                                           int* __restrict__ cs, int* __restrict__ list) {
+                                                           int chains, int cut, int link,
+                                                           int64_t slots, int* __restrict__ cs,
+                                                           int* __restrict__ list) {
   __shared__ int part[NTB / 64], from[64], total, longest, used;
   const int tid = threadIdx.x, lane = tid & 63, per = (nseq + NTB - 1) / NTB;
   const int s0 = min(nseq, tid * per), s1 = min(nseq, s0 + per);
@@ -728,7 +729,13 @@ __global__ __launch_bounds__(NTB) void lina_offsets_kernel(const int* __restrict
     atomicMax(&longest, top);
   }
   __syncthreads();
-  L = (int64_t)longest * cut > (int64_t)total * chains ? least : max(least, longest);  // cut 160: 1.6 shares of 256
+  // Links: a chain of n chunks in segments of L takes 1.7 L steps of both walks and (n - 1) / L links, which L = sqrt(link n)
+  // balances; with the second walk's start, twice L and the links have to be less than n.  16 chunks, d = 128: 64 us
+  // whole, 69 cut; 20: 76 and 77; 24: 86 and 76.
+  const int seg = max(least, (int)ceilf(sqrtf(0.1f * (float)link * (float)longest)));
+  const bool segs = (int64_t)longest * cut > (int64_t)total * chains &&  // cut 160: 1.6 shares of 256
+                    (link == 0 || 2.f * ((float)seg + 0.1f * (float)(link * ((longest - 1) / seg))) < (float)longest);
+  L = segs ? seg : max(least, longest);
   if (tid == 0) cs[nseq + 1] = L;
   auto cls = [&](int len) { return 63 - (int)((int64_t)len * 63 / L); };
   each([&](int i, int end, int nch, int nsg) {
@@ -931,8 +938,8 @@ hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv) {
 }
 
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int chains, int* cs, int* list, void* stream,
-                               int cut) {
-  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, L, chains, cut,
+                               int cut, int link) {
+  hipLaunchKernelGGL(lina_offsets_kernel, dim3(1), dim3(NTB), 0, (hipStream_t)stream, cu, n, T, L, chains, cut, link,
                      lina_pieces(T, n, L), cs, list);
   return hipGetLastError();
 }

@@ -570,3 +570,38 @@ def test_other_sequences_keep_their_results():
     assert torch.equal(o[1], o2[1]) and torch.equal(o[0, :, 1], o2[0, :, 1]) and torch.equal(o[0, :128, 0], o2[0, :128, 0])
     assert torch.equal(s[1], s2[1]) and torch.equal(s[0, 1], s2[0, 1])
     assert bool(torch.isnan(o2[0, 150:, 0]).all()) and bool(torch.isnan(s2[0, 0]).all())
+
+
+@pytest.mark.parametrize("H,dk,dv,T,dtype,most", [(1, 128, 64, 131072, "bf16", 64), (1, 128, 128, 131072, "bf16", 64),
+                                                  (2, 64, 64, 32768, "bf16", 64), (1, 128, 128, 9000, "f32", 24),
+                                                  (1, 64, 128, 1200, "bf16", 3), (1, 64, 128, 700, "bf16", 1),
+                                                  (1, 128, 64, 1000, "f32", 1)])  # 2 (8 + 0.5) steps against 16
+def test_few_packed_chains_have_few_links(H, dk, dv, T, dtype, most):
+    """Segments of one long packed sequence are joined one after another, so that there are about as many as a segment has
+    chunks, at most 2.5 times the root of all; and a short one is walked whole.  The offsets kernel leaves 0, T
+    and a segment's chunks at the end of the workspace.  The results are those of the sequence unpacked."""
+    import torch
+    import gated_delta_rule_78_amd as kda
+    from gated_delta_rule_78_amd.gdr import _planned
+    g = torch.Generator(device="cuda").manual_seed(7)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    unit = lambda *s: torch.nn.functional.normalize(rn(*s), dim=-1).to(dt)
+    q, k, v, b = unit(1, T, H, dk), unit(1, T, H, dk), rn(1, T, H, dv).to(dt), torch.sigmoid(rn(1, T, H)).to(dt)
+    gl = -0.1 * torch.rand(1, T, H, generator=g, device="cuda")
+    s0 = rn(1, H, dk, dv)
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(_planned(q, k, v, gl, b, 1)[-1], dtype=torch.uint8, device="cuda")
+    o, s = kda.gdr_chunk_fwd(q, k, v, gl, b, initial_state=s0, cu_seqlens=cu, workspace=ws)
+    tail = ws[-65536:].view(torch.int32).tolist() if ws.numel() >= 65536 else ws.view(torch.int32).tolist()
+    at = [i for i in range(len(tail) - 2) if tail[i] == 0 and tail[i + 1] == T]
+    chunks = -(-T // 64)
+    segments = {-(-chunks // tail[i + 2]) for i in at if tail[i + 2] > 0}
+    assert segments and max(segments) <= min(most, max(1, 2.5 * chunks ** 0.5)), segments
+    r, rs = kda.gdr_chunk_fwd(q, k, v, gl, b, initial_state=s0)
+    _rel(s, _np(rs), 2 * _fp32(T), "final state", 1.0, (2, 3))
+    if dtype == "bf16":  # two roundings of values that differ by fp32's bound: a step at most
+        x, y = _np(o), _np(r)
+        assert (np.abs(x - y) <= 2.0 ** -7 * np.abs(y) + 2 * (3 * 2.0 ** -16 + _fp32(T)) * 8).all()
+    else:
+        _rel(o, _np(r), 2 * _fp32(T), "o", 0.1 * np.sqrt(T))
