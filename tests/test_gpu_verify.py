@@ -155,3 +155,28 @@ def test_a_round_of_drafting(dtype):
         assert torch.equal(ot[keep], o[:, t][keep])
     assert torch.equal(one, S)
     assert bool((n >= 0).all()) and bool((n <= K).all()) and bool((token >= 0).all()) and len(set(n.tolist())) > 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sure", [False, True])
+@pytest.mark.parametrize("B,K,V", [(700, 1, 5 * 2048 + 1), (500, 2, 9 * 2048 - 7), (2100, 1, 3 * 2048 + 5)])
+def test_workgroups_of_several_tiles(B, K, V, sure, dtype):
+    """Many sequences share the workgroups, so that one goes through several tiles of a row, the last round of them not all
+    there: 6 tiles by 2 workgroups, 9 by 4, 4 by one.  Some drafts are padding."""
+    import torch
+    p, x, q, u, ul = _case(B, K, V, dtype, B + V, sure)
+    x[::7, K - 1] = -1
+    ul[:4] = torch.tensor([0.0, 1.0 - 2.0 ** -24, 0.999, 0.5])
+    n, t = _check(p, x, q, u, ul)
+    assert len(set((t // 2048).tolist())) == -(-V // 2048)  # every tile has been drawn from
+
+
+def test_the_one_index_that_weighs_anything():
+    """A refused draft; of the target's row one index alone weighs anything, in the second tile."""
+    import torch
+    p, x, q, u, ul = _case(3, 2, 2500, seed=5)
+    x[:, 0] = torch.tensor([3, 2399, 2401])
+    p[:, 0] = 0.0
+    p[:, 0, 2400] = 1.0
+    n, t = _check(p, x, q, torch.ones_like(u), ul)
+    assert list(n) == [0, 0, 0] and list(t) == [2400] * 3
