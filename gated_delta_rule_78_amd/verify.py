@@ -43,7 +43,8 @@ def verify_drafts(target_probs, drafts, draft_probs, u, u_next, workspace=None):
     last; drafts int32 [B,K]: an index outside [0, V) ends a sequence's drafts (padding);
     draft_probs [B,K,V] in the dtype of target_probs: the distributions they were drawn from, or None
     where they were chosen outright (all of q on the draft); u fp32 [B,K], u_next fp32 [B]: random numbers
-    in [0, 1).  Entries that are negative or not finite weigh nothing; where no weight is left after a
+    in [0, 1).  Whether a draft stands is u q < p of these entries as they are (a NaN refuses).  As weights,
+    entries that are negative or not finite count nothing; where no weight is left after a
     refusal, the token is drawn from the target's row itself, and it is -1 if that weighs nothing.
     Returns (accepted int32 [B], next_token int32 [B])."""
     torch = _kda._torch()

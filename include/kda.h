@@ -600,8 +600,10 @@ int kda_gdr_decode_tokens(const kda_shape* shape, int qk_heads, const int* count
  *                  first or the last index that weighs anything)
  *   accepted, next_token : [B] int32 outputs
  *   workspace    : the size below, 8-byte aligned
- * Entries that are negative or not finite weigh nothing (a NaN never lets a draft stand).  Weights that are
- * all zero after a refusal give way to p_n; next_token is -1 where that weighs nothing either.
+ * Weights: entries that are negative or not finite weigh nothing; weights that are all zero after a refusal
+ * give way to p_n, and next_token is -1 where that weighs nothing either.  The comparison takes u, p and q as they
+ * are: on a p of infinity a draft stands unless u q is infinite too, a q under zero lets one stand on a p of zero, and a NaN
+ * in any of the three, or nothing times infinity, refuses.
  * Alignment: the elements'.  No output may overlap an input, another output or the workspace.  K or V over
  * 2^30, more than 2^31 rows of p, 2^59 probabilities or 2^24 pieces of 2,048 tokens are KDA_ERR_SHAPE.
  */

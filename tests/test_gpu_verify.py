@@ -180,3 +180,17 @@ def test_the_one_index_that_weighs_anything():
     p[:, 0, 2400] = 1.0
     n, t = _check(p, x, q, torch.ones_like(u), ul)
     assert list(n) == [0, 0, 0] and list(t) == [2400] * 3
+
+
+def test_odd_entries_at_the_drafts():
+    """The rule that lets a draft stand takes the entries as they are: u q < p in fp64."""
+    import torch
+    inf, nan = float("inf"), float("nan")
+    rows = [(0.5, inf, 0.5, 1), (0.5, 0.1, -1.0, 1), (0.5, 0.0, -1.0, 1), (0.5, -0.1, -1.0, 1), (0.5, -1.0, 0.5, 0),
+            (0.5, 0.9, inf, 0), (0.0, 0.9, inf, 0), (0.5, nan, 0.5, 0), (0.5, 0.5, nan, 0), (0.0, nan, nan, 0), (0.0, 0.0, 0.5, 0),
+            (0.5, inf, inf, 0), (nan, 0.5, 0.5, 0)]
+    p, x, q, u, ul = _case(len(rows), 1, 300, seed=6)
+    for i, (a, px, qx, _) in enumerate(rows):
+        u[i, 0], p[i, 0, x[i, 0]], q[i, 0, x[i, 0]] = a, px, qx
+    n, _ = _check(p, x, q, u, ul)
+    assert list(n) == [r[3] for r in rows]
