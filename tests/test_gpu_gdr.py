@@ -605,3 +605,83 @@ def test_few_packed_chains_have_few_links(H, dk, dv, T, dtype, most):
         assert (np.abs(x - y) <= 2.0 ** -7 * np.abs(y) + 2 * (3 * 2.0 ** -16 + _fp32(T)) * 8).all()
     else:
         _rel(o, _np(r), 2 * _fp32(T), "o", 0.1 * np.sqrt(T))
+
+
+def _rounded_dq_dk(q, k, v, g, b, do, S0, dS, scores=lambda x: x):
+    """dq and dk in fp64 with a rounding to bf16 where the kernels have one: the state S that a chunk meets, the gradient R
+    of the state behind it, r = v - e^g S^T k, y = dv, and the results.  scores: what a score is taken as."""
+    import torch
+    bf = lambda x: torch.from_numpy(np.ascontiguousarray(x)).float().bfloat16().double().numpy()
+    B, T, Hk, dk = q.shape
+    H, dv, C = *v.shape[2:], 64
+    dq, dkk = np.zeros((B, T, H, dk)), np.zeros((B, T, H, dk))
+    ys = ref.gdr_bwd(q, k, v, g, b, do, S0, dS)[2]
+    for i, h in np.ndindex(B, H):
+        Q, K, V, G, be, D, Y = (x[i, :, j] for x, j in ((q, h * Hk // H), (k, h * Hk // H), (v, h), (g, h), (b, h), (do, h), (ys, h)))
+        S, R = (np.zeros((dk, dv)) if x is None else x[i, h] for x in (S0, dS))
+        starts, behind, r = {}, {}, np.zeros((T, dv))
+        for t in range(T):
+            if t % C == 0:
+                starts[t // C] = bf(S)
+            S = np.exp(G[t]) * S
+            r[t] = V[t] - S.T @ K[t]
+            S = S + np.outer(K[t], be[t] * r[t])
+        for t in range(T - 1, -1, -1):
+            if t == T - 1 or (t + 1) % C == 0:
+                behind[t // C] = bf(R)
+            R = (np.exp(G[t + 1]) if t + 1 < T else 1.0) * R + np.outer(Q[t], D[t]) - np.outer(K[t], Y[t])
+        for c in starts:
+            s = slice(c * C, min(T, c * C + C))
+            sums = np.cumsum(G[s])
+            end = sums[-1] + (G[s.stop] if s.stop < T else 0.0)  # with the next token's decay
+            low = np.tril(np.exp(np.minimum(sums[:, None] - sums, 0.0)))
+            u, y, eg = be[s, None] * bf(r[s]), bf(Y[s]), np.exp(sums)[:, None]
+            E, F = scores(low * (D[s] @ u.T)), scores(np.tril(low * (y @ u.T), -1))
+            dq[i, s, h] = E @ K[s] + eg * (D[s] @ starts[c].T)
+            dkk[i, s, h] = E.T @ Q[s] - (F + F.T) @ K[s] - eg * (y @ starts[c].T) + np.exp(end - sums)[:, None] * (u @ behind[c].T)
+    share = lambda x: bf(x.reshape(B, T, Hk, H // Hk, dk).sum(3))
+    return share(dq), share(dkk)
+
+
+# B, T, Hk, H, dk, dv, start states and gradients of the last ones, largest beta
+ROUNDED = [(1, 400, 2, 2, 128, 128, True, 1.0), (1, 400, 2, 4, 64, 64, True, 2.0), (1, 300, 4, 4, 64, 128, False, 1.0),
+           (2, 200, 2, 4, 128, 64, True, 1.0)]
+
+
+def _rounded_case(B, T, Hk, H, dk, dv, states, beta):
+    import torch
+    ins = _inputs(B, T, Hk, H, dk, dv, "bf16", T + dv, beta)
+    gen = torch.Generator().manual_seed(dk)
+    S0, dS = (torch.randn(B, H, dk, dv, generator=gen) for _ in range(2)) if states else (None, None)
+    return ins, S0, dS
+
+
+@pytest.mark.parametrize("B,T,Hk,H,dk,dv,states,beta", ROUNDED)
+def test_gradients_of_q_and_k_take_no_other_roundings(B, T, Hk, H, dk, dv, states, beta):
+    """bf16 inputs: dq and dk as fp64 gives them with the roundings that are named, and their distance from the formula's.
+
+    From it: each of a sum's products has roundings of its own in one operand (dq: d_o S^T in S, E K in r) or two (dk:
+    y S^T, F in y and r, u R^T), independent ones of at most 2^-8 / sqrt(3) in the root mean square, and the result has
+    one: sqrt(2) 2^-8 / sqrt(3) and 2^-8 of the norm.  To the rounded form: an operand that is off by a share d before it
+    is rounded to bf16 falls on the other side in d / step of all cases and is then a step off, sqrt(d step) in the
+    root mean square with a step of up to 2^-7.  d is fp32's bound (_fp32, up to 8e-6 here) for the four operands, and 2^-16 of
+    the scores for the result: (4 . 8e-6 2^-7 + 2^-16 2^-7)^(1/2) = 6.1e-4, within 2^-10."""
+    import gated_delta_rule_78_amd as kda
+    ins, S0, dS = _rounded_case(B, T, Hk, H, dk, dv, states, beta)
+    out = kda.gdr_chunk_bwd(*_dev(*ins), initial_state=_dev(S0)[0], d_final_state=_dev(dS)[0])
+    x = [_np(y) for y in ins]
+    want, near = ref.gdr_bwd(*x, _np(S0), _np(dS)), _rounded_dq_dk(*x, _np(S0), _np(dS))
+    for i, (name, bound) in enumerate((("dq", 2.0 ** -8 * np.sqrt(2 / 3)), ("dk", 2.0 ** -8))):
+        _rel(out[i], want[i], bound, name)
+        _rel(out[i], near[i], 2.0 ** -10, name + " as rounded")
+
+
+def test_rounded_gradients_tell_scores_of_fewer_bits():
+    """The bound to the rounded form is one that scores of 8 bits do not keep."""
+    import torch
+    bf = lambda x: torch.from_numpy(np.ascontiguousarray(x)).float().bfloat16().double().numpy()
+    for case in ROUNDED:
+        ins, S0, dS = _rounded_case(*case)
+        x = [_np(y) for y in ins]
+        good, bad = _rounded_dq_dk(*x, _np(S0), _np(dS)), _rounded_dq_dk(*x, _np(S0), _np(dS), bf)
+        assert all((_norm(b - a, (1, 3)) / _norm(a, (1, 3))).max() > 2.0 ** -10 for a, b in zip(good, bad)), case
