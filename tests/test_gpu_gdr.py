@@ -685,3 +685,64 @@ def test_rounded_gradients_tell_scores_of_fewer_bits():
         x = [_np(y) for y in ins]
         good, bad = _rounded_dq_dk(*x, _np(S0), _np(dS)), _rounded_dq_dk(*x, _np(S0), _np(dS), bf)
         assert all((_norm(b - a, (1, 3)) / _norm(a, (1, 3))).max() > 2.0 ** -10 for a, b in zip(good, bad)), case
+
+
+def test_decode_of_prepared_queries_and_keys():
+    import torch
+    import gated_delta_rule_78_amd as kda
+    q, k, v, g, b, _ = (x[:, 0].contiguous() for x in _dev(*_inputs(3, 2, 2, 4, 64, 128, "bf16")))
+    q, k = 3 * q, 2 * k
+    qn, kn = (x[:, 0].contiguous() for x in kda.qk_norm_rope(q[:, None].contiguous(), k[:, None].contiguous(), norm="l2"))
+    S = torch.randn(3, 4, 64, 128, device="cuda")
+    a, c = S.clone(), S.clone()
+    o = kda.gdr_decode_step(q, k, v, g, b, a, qk_prep=dict(norm="l2"))
+    assert torch.equal(o, kda.gdr_decode_step(qn, kn, v, g, b, c)) and torch.equal(a, c) and not torch.equal(a, S)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [700, 9000])
+def test_packed_workspace_may_hold_anything(T, dtype):
+    """Slots that no chunk, segment or token of a packed batch needs are not read: NaN patterns in all of the workspace."""
+    import torch
+    import gated_delta_rule_78_amd as kda
+    from gated_delta_rule_78_amd.gdr import _planned
+    ins = _dev(*_inputs(1, T, 1, 2, 64, 64, dtype))
+    cu = _cu(T)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    for bwd in (False, True):
+        call = (lambda **kw: kda.gdr_chunk_bwd(*ins, cu_seqlens=c, **kw)) if bwd else (
+            lambda **kw: kda.gdr_chunk_fwd(*ins[:5], cu_seqlens=c, out=torch.zeros_like(ins[2]), **kw))
+        need = _planned(*ins[:5], len(cu) - 1, bwd)[-1]
+        zeros, ws = torch.zeros(need, dtype=torch.uint8, device="cuda"), torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+        for x, y in zip(call(workspace=zeros), call(workspace=ws[:need])):
+            assert torch.equal(x, y)
+        assert bool((ws[need:] == 0xFF).all())
+
+
+def test_decode_captured_and_replayed():
+    """A round of drafting in a captured graph: outputs with the state left alone, then the state over the counted tokens."""
+    import torch
+    import gated_delta_rule_78_amd as kda
+    ins = _dev(*_inputs(3, 5, 2, 4, 64, 128, "bf16")[:5])
+    S, c = torch.zeros(3, 4, 64, 128, device="cuda"), torch.tensor([5, 0, 2], dtype=torch.int32, device="cuda")
+
+    def call(x, S, c):
+        o = kda.gdr_decode_tokens(*x, S, update=False)
+        kda.gdr_decode_tokens(None, *x[1:], S, counts=c)
+        return o
+
+    call(ins, S, c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(ins, S, c)
+    S.zero_()
+    T = torch.zeros_like(S)
+    for seed in (1, 2, 3):
+        new, n = _dev(*_inputs(3, 5, 2, 4, 64, 128, "bf16", seed)[:5]), torch.tensor([seed, 5, 0], dtype=torch.int32, device="cuda")
+        want = call(new, T, n)
+        for a, b in zip((*ins, c), (*new, n)):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(S, T)
