@@ -746,3 +746,16 @@ def test_decode_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(S, T)
+
+
+def test_packed_batch_of_no_tokens():
+    """Sequences without a token hand their states on, both ways."""
+    import torch
+    import gated_delta_rule_78_amd as kda
+    z = lambda *s: torch.zeros(*s, device="cuda")
+    ins = (z(1, 0, 2, 64), z(1, 0, 2, 64), z(1, 0, 4, 128), z(1, 0, 4), z(1, 0, 4))
+    s = torch.randn(3, 4, 64, 128, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert torch.equal(kda.gdr_chunk_fwd(*ins, initial_state=s, cu_seqlens=cu)[1], s)
+    assert torch.equal(kda.gdr_chunk_bwd(*ins, ins[2], d_final_state=s, cu_seqlens=cu)[5], s)
+    assert kda.gdr_chunk_fwd(*ins, cu_seqlens=cu[:1])[1].shape == (0, 4, 64, 128)
