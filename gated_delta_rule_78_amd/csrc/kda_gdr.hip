@@ -72,7 +72,7 @@ struct PrepLds {
   float blk[4][SUB][SUB + 4];  // one 16 x 16 block of each row group
 };
 
-// X = (I - M)^-1 of four strictly lower 16 x 16 blocks at once, -M's rows in `blk`: row group r of the wave
+// X = (I - M)^-1 of four strictly lower 16 x 16 blocks at once, M's rows in `blk`: row group r of the wave
 // takes block r, lane n its column n, by forward substitution (bounded by X's own size, which the powers
 // of M are not: for equal keys they grow like binomials).  X's rows replace M's.
 __device__ __forceinline__ void invert_blocks(float (&blk)[4][SUB][SUB + 4], int lane) {
@@ -110,8 +110,8 @@ __device__ __forceinline__ void mm16(f32x4_t& acc, const f32x4_t& x, const f32x4
 }
 
 // One wave: N and P of one chunk and head, fp32.  A wave each, without barriers, three workgroups to a compute unit (bf16).
-// What bounds it: N and P are 20 KB of fp32 written for 32 KB of bf16 q and k read (d = 128), and the substitution is a chain
-// of 16 dependent rows.  B4 H32 T8K 170 us, H16 T128K 331.
+// What bounds it: bytes.  N and P are 20 KB of fp32 written for 32 KB of bf16 q and k read (d = 128): B4 H32 T8K 0.94 GB
+// in 170 us, 5.5 TB/s (matrix cores 15% busy), H16 T128K 331.  Scores of shared heads are made for every value head.
 template <typename T, int DK, bool REV>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void gdr_prep_kernel(const GdrParams gp) {
   constexpr int KS = DK / 32;
@@ -343,11 +343,13 @@ static_assert(sizeof(TokenLds) == kTokenFloats * 4, "as in memory");
 // outputs, which are rounded to bf16 themselves, take S, P and b o r in two (16 bits).
 //
 // What bounds it: the chain from S through K S, r and b o r back to S.  A step of the forward (d = 128, bf16) has 182 products
-// a wave and takes 6,400 to 6,700 cycles, matrix units 35 to 38% busy; conflict-free tiles, another order and other ways to
-// split changed it by a few percent.  B4 H32 T8K: 409 us for 128 steps in a row; in training 629 forward, 800 in reverse, where
-// states and r are written too and the products of Q and d_o come on top.  Of 131,072 tokens, 16 heads (32 chains): end states
-// and transfers of segments 1,075 us, links 63, outputs 779.  Two workgroups to a compute unit in the first pass (128
-// registers) spill: 4,260 us for the whole call instead of 2,227.
+// a wave and takes about 6,900 cycles, matrix cores 42% busy; tiles of fewer LDS conflicts, another order and other ways to
+// split changed it by a few percent.  B4 H32 T8K: 409 to 419 us for 128 steps in a row; in training 634 forward (36% busy), 811
+// in reverse (26%), where states and r are written too and the products of Q and d_o come on top.  Of 131,072 tokens, 16 heads
+// (32 chains): end states and transfers of segments 1,075 us, links 63, outputs 780.  Two workgroups to a compute unit in the first
+// pass (128 registers) spill: 4,260 us for the whole call instead of 2,227.
+// Registers: all 256 are in use in training, and some do not fit: bf16, d = 128 in reverse 51 (208 bytes of scratch a
+// lane); fp32, d = 128 5 in the forward, 31 in training, 192 in reverse (772 bytes) and 60 in its first pass; d = 64 11 in reverse.
 template <typename T, int DK, int MODE>
 __global__ __launch_bounds__(2 * NT, 2) void gdr_walk_kernel(const GdrParams gp) {
   typedef WalkLds<T, DK, MODE> Lds;

@@ -45,7 +45,7 @@ int segment_override() {
 
 // A chain (sequence, head, 64 value columns) is walked in order.  With few chains it is cut into segments,
 // which costs a first pass over all but the last (the value columns and the transfer's, about 0.7 of a
-// step each) and the links between them (about 1.5 steps each, one after another); a cut is taken where this sum of steps on
+// step each) and the links between them (counted as 1.5 steps each, one after another); a cut is taken where this sum of steps on
 // 256 compute units is least.  As it chooses, whole and in segments of 16 chunks: 131,072 tokens, 16 heads 2,205, 5,698 and
 // 3,602 us; 8,192 tokens, 16 heads 206, 370 and 206; 2 x 8,192, 32 heads 429, 431 (whole) and 607; 2,048 tokens, 8 heads 103,
 // 108 and 113.  Packed chains are cut, or not, where their lengths are known

@@ -8,9 +8,9 @@
 // One workgroup makes dq and dk of one chunk and shared head, summed over the heads it serves in registers: wave
 // w block w of 16 tokens, in 16 x 16 tiles with rows = channels, columns = tokens, so that a lane stores four
 // neighbouring channels.  Operands go through LDS, 64 value columns at a time, the
-// two states one after the other through the same tile: 72 KB (bf16), two workgroups to a compute unit.  B4 H32 T8K: 728 us
-// (one workgroup to a unit, both states at once: 1,034) for 1.07 GB of states and 1.9 GB of rows: loads and products take turns
-// between barriers.  Scores are split in two terms: in one, dk is off by 3.4e-3 of its norm instead of 2.8e-3.
+// two states one after the other through the same tile: 72 KB (bf16), two workgroups to a compute unit, for which 10
+// registers do not fit (44 bytes of scratch a lane).  B4 H32 T8K: 727 us (one workgroup to a unit, both states at once: 1,034) for
+// 2.5 GB read, 1.07 of them states, and 0.7 written, 4.4 TB/s: loads and products take turns between barriers.  Scores are split in two terms: in one, dk is off by 3.4e-3 of its norm instead of 2.8e-3.
 #include "kda_gdr_tile.h"
 
 namespace kda {

@@ -3,13 +3,17 @@
 //
 // Draft x_i stands while u_i q_i(x_i) < p_i(x_i).  After n of them the next token is drawn from
 // max(p_n - q_n, 0) where a draft was refused, from p_n where none was left: the lowest index whose running
-// sum passes u_next times the whole.  All of it in fp64, so that the index does not hang on the order of a sum.
+// sum passes u_next times the whole.  All of it in fp64, so that only a u_next within about 1e-13 of a border
+// between two indices could tell two orders of summation apart.
 //
 // Only row n of p and q is read whole, in tiles of 2,048 tokens: the first kernel sums each tile (weights, and p's
 // own, for where the weights are all zero), the second finds the tile and the token in it.  What both wait for is one
 // access to memory after another: the drafts, their probabilities, the row; so a workgroup of the first goes through several
-// tiles of a row once it knows which.  128 sequences over 131,072 tokens, fp32 (134 MB of p and q where a draft is refused):
-// 31 us, 4.4 TB/s, and 9 for the second kernel; a single sequence 5 and 9, latency.  Tiles of 4,096 tokens were slower.
+// tiles of a row once it knows which.  128 sequences over 131,072 tokens, fp32 (105 MB: p of all, q of the 54%
+// that had a draft refused): 30 us, 3.5 TB/s, and 9 for the second kernel, 33.7 together; with every one refused (134 MB) 38.7:
+// further bytes go at 5.8 TB/s, the rest is those accesses and the second kernel.  Drafts chosen outright (67 MB) 30.0; bf16
+// rows (52 MB) 55.6, because a guarded load and its widening stand together, so that a thread's loads wait for each other (36 waits in the
+// kernel's code, fp32 has 5).  A single sequence 5 and 9, latency.  Tiles of 4,096 tokens were slower.
 #include <math.h>
 
 #include "kda_common.h"

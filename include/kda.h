@@ -593,7 +593,8 @@ int kda_gdr_decode_tokens(const kda_shape* shape, int qk_heads, const int* count
  *   u_i q_i(x_i) < p_i(x_i) ;
  * with n of them standing the next token is the lowest index whose running sum of weights passes
  * u_next times their whole; the weights are max(p_n - q_n, 0) where draft n was refused, p_n where
- * there is none (n == K, or x_n outside [0, V): padding).  All sums and products are fp64.
+ * there is none (n == K, or x_n outside [0, V): padding).  All sums and products are fp64: only a
+ * u_next within about 1e-13 of a border between two indices could fall on either side.
  *   target_probs : [B, K + 1, V] p in dtype;  draft_probs : [B, K, V] q in dtype, or NULL: all of q_i
  *                  is on x_i
  *   drafts       : [B, K] int32;  u : [B, K], u_next : [B] fp32 in [0, 1) (a u_next outside draws the
