@@ -77,8 +77,8 @@ hipError_t launch_lina_walk(const LinaWalk& w);
 hipError_t launch_lina_pair(const LinaWalk& wq, const LinaWalk& wv);
 // dk's and dv's walk in one kernel: bf16, widths equal; wv.x: v
 hipError_t launch_lina_reverse(const LinaWalk& wk, const LinaWalk& wv);
-// chains: of a sequence; a batch is cut where its longest chain is over 256 / cut shares of all steps; link: tenths of a
-// segment's step that joining two segments takes, where they are joined one after another (0: they are not)
+// chains: of a sequence; a batch is cut where its longest chain is over 256 / cut shares of all steps; link: tenths of what
+// both walks of a chunk take that joining two segments does, where they are joined one after another (0: they are not)
 hipError_t launch_lina_offsets(const int* cu, int n, int T, int L, int chains, int* cs, int* list, void* stream,
                                int cut = 160, int link = 0);
 hipError_t launch_lina_headsum(const float* part, void* out, int64_t rows, int heads, int group, int d, bool bf16,
